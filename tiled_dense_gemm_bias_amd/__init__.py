@@ -588,3 +588,12 @@ def cache_store(arch, cus, M, N, K, sched: dict, ms: float, act="gelu", dtype="f
     if st not in (0, 10):
         raise GbaError(st, "gba_cache_store")
     return st
+
+
+# Products grouped by expert and 4-bit floats (libgba_experts.so, loaded at the
+# first call).
+from .experts import (  # noqa: E402,F401
+    gemm_bias_act_mx4, grouped_gemm_act_grad, grouped_gemm_bias_act, grouped_gemm_bias_act_mx4,
+    grouped_gemm_wgrad, mx4_dequantize, mx4_pack_scales, mx4_quantize, mx4_scales_shape,
+    mx4_unpack_scales,
+)

@@ -1,0 +1,317 @@
+// C ABI of libgba_experts (declared in gba_experts.h): argument checks, device
+// check, choice of kernel, launch.
+#include <string.h>
+
+#include <mutex>
+
+#include "gba_experts.h"
+#include "gx_launch.hpp"
+#include "gx_mx4.hpp"
+#include "gx_colsum.hpp"
+
+#define GBX_VERSION_STRING "0.1.0"
+
+namespace {
+
+thread_local hipStream_t t_stream = nullptr;
+thread_local int t_last_hip = 0;
+
+int hip_result(hipError_t e) {
+    if (e == hipSuccess) return GBA_OK;
+    t_last_hip = (int)e;
+    return GBA_ERR_HIP;
+}
+
+// GBA_OK when the current device is a gfx950.
+int check_device() {
+    static std::mutex mu;
+    static int state[64];   // 0: not looked at, 1: gfx950, 2: another
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess || dev < 0 || dev >= 64) {
+        (void)hipGetLastError();
+        t_last_hip = (int)e;
+        return GBA_ERR_DEVICE;
+    }
+    std::lock_guard<std::mutex> lk(mu);
+    if (!state[dev]) {
+        hipDeviceProp_t p;
+        e = hipGetDeviceProperties(&p, dev);
+        if (e != hipSuccess) {
+            (void)hipGetLastError();
+            t_last_hip = (int)e;
+            return GBA_ERR_DEVICE;
+        }
+        state[dev] = strncmp(p.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
+    }
+    return state[dev] == 1 ? GBA_OK : GBA_ERR_DEVICE;
+}
+
+// ------------------------------------------------------------ argument checks --
+
+// An array argument: where it is, how long, how it must be aligned.
+struct Span {
+    const void *p;
+    size_t bytes;
+    bool required, output;
+    unsigned align;
+};
+
+bool overlap(const Span &a, const Span &b) {
+    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x < y + b.bytes && y < x + a.bytes;
+}
+
+template <int N>
+int check_spans(const Span (&s)[N]) {
+    for (const Span &a : s)
+        if (a.required && a.bytes && !a.p) return GBA_ERR_NULL;
+    for (const Span &a : s)
+        if (a.p && ((uintptr_t)a.p & (a.align - 1))) return GBA_ERR_ALIGN;
+    for (int i = 0; i < N; ++i)
+        for (int j = 0; j < N; ++j)
+            if (i != j && s[i].output && overlap(s[i], s[j])) return GBA_ERR_ALIAS;
+    return GBA_OK;
+}
+
+int check_enums(int act, int dtype) {
+    if (dtype != GBA_DTYPE_F16 && dtype != GBA_DTYPE_BF16) return GBA_ERR_DTYPE;
+    if (act < GBA_ACT_NONE || act > GBA_ACT_GELU_TANH) return GBA_ERR_ACT;
+    return GBA_OK;
+}
+
+constexpr int64_t kMaxRows = 0x7fffffffLL;
+// A row pitch inside a tile's 32-bit byte offsets: 256 K-contiguous rows, or 64 rows along K.
+constexpr int64_t kMaxDepth = 1LL << 21, kMaxWidth = 1LL << 23;
+
+int check_sizes(int64_t T, int64_t E, int64_t depth, int64_t width) {
+    if (T < 0 || depth < 0 || width < 0 || E < 1 || E > GBX_MAX_EXPERTS) return GBA_ERR_SHAPE;
+    if (T > kMaxRows || depth > kMaxDepth || width > kMaxWidth) return GBA_ERR_SHAPE;
+    return GBA_OK;
+}
+
+size_t size3(int64_t a, int64_t b, int64_t c) { return (size_t)a * (size_t)b * (size_t)c; }
+
+// Tile for rows of about T / E an expert.
+int row_tile(int64_t T, int64_t E) {
+    const int64_t mean = T / (E < T ? E : T);
+    return mean <= 16 ? gbx::TILE_16x64 : mean <= 96 ? gbx::TILE_64x64 : gbx::TILE_128x128;
+}
+
+}  // namespace
+
+extern "C" {
+
+const char *gbx_version(void) { return GBX_VERSION_STRING; }
+int gbx_last_hip_error(void) { return t_last_hip; }
+int gbx_set_stream(void *s) {
+    t_stream = (hipStream_t)s;
+    return GBA_OK;
+}
+
+int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, const void *bias,
+                          void *C, void *preact, int64_t T, int64_t E, int64_t N, int64_t K,
+                          int act, int dtype, int flags, void *workspace, size_t workspace_bytes) {
+    int s = check_enums(act, dtype);
+    if (s) return s;
+    if (flags & ~GBA_TRANSPOSE_B) return GBA_ERR_SHAPE;
+    if ((s = check_sizes(T, E, K, N))) return s;
+    if ((K % 8) || (N % 8)) return GBA_ERR_ALIGN;
+    const Span spans[] = {{A, size3(T, K, 2), true, false, 16},
+                          {offsets, (size_t)(E + 1) * 4, T > 0 && N > 0, false, 4},
+                          {W, size3(E, N * 2, K), T > 0, false, 16},
+                          {bias, size3(E, N, 2), false, false, 16},
+                          {C, size3(T, N, 2), true, true, 16},
+                          {preact, size3(T, N, 2), false, true, 16},
+                          {workspace, workspace_bytes, false, true, 16}};
+    if ((s = check_spans(spans))) return s;
+    if (T == 0 || N == 0) return GBA_OK;
+    if ((s = check_device())) return s;
+    gbx::Group g = {};
+    g.A = (const uint16_t *)A;
+    g.B = (const uint16_t *)W;
+    g.offsets = offsets;
+    g.bias = (const uint16_t *)bias;
+    g.C = C;
+    g.zout = (uint16_t *)preact;
+    g.T = (int)T;
+    g.E = (int)E;
+    g.N = (int)N;
+    g.K = (int)K;
+    g.act = act;
+    g.splits = 1;
+    return hip_result(((flags & GBA_TRANSPOSE_B) ? gbx::fwd_nt : gbx::fwd_nn)[dtype][row_tile(T, E)](g, t_stream));
+}
+
+int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W, const void *z,
+                          void *dA, int64_t T, int64_t E, int64_t N, int64_t K, int act, int dtype,
+                          int flags, void *workspace, size_t workspace_bytes) {
+    int s = check_enums(act, dtype);
+    if (s) return s;
+    if (flags & ~GBA_TRANSPOSE_B) return GBA_ERR_SHAPE;
+    if ((s = check_sizes(T, E, N, K))) return s;
+    if ((K % 8) || (N % 8)) return GBA_ERR_ALIGN;
+    const Span spans[] = {{dC, size3(T, N, 2), true, false, 16},
+                          {offsets, (size_t)(E + 1) * 4, T > 0 && K > 0, false, 4},
+                          {W, size3(E, N * 2, K), T > 0, false, 16},
+                          {z, size3(T, K, 2), act != GBA_ACT_NONE, false, 16},
+                          {dA, size3(T, K, 2), true, true, 16},
+                          {workspace, workspace_bytes, false, true, 16}};
+    if ((s = check_spans(spans))) return s;
+    if (T == 0 || K == 0) return GBA_OK;
+    if ((s = check_device())) return s;
+    gbx::Group g = {};
+    g.A = (const uint16_t *)dC;
+    g.B = (const uint16_t *)W;
+    g.offsets = offsets;
+    g.z = (const uint16_t *)z;
+    g.C = dA;
+    g.T = (int)T;
+    g.E = (int)E;
+    g.N = (int)K;   // the product's columns
+    g.K = (int)N;   // and its depth
+    g.act = act;
+    g.splits = 1;
+    // W [E,N,K] has its rows along the sum, W [E,K,N] its columns.
+    return hip_result(((flags & GBA_TRANSPOSE_B) ? gbx::slope_nn : gbx::slope_nt)[dtype][row_tile(T, E)](g, t_stream));
+}
+
+int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, void *dW,
+                       void *dbias, int64_t T, int64_t E, int64_t N, int64_t K, int dtype,
+                       int flags, void *workspace, size_t workspace_bytes) {
+    int s = check_enums(GBA_ACT_NONE, dtype);
+    if (s) return s;
+    if (flags & ~(GBA_TRANSPOSE_B | GBX_OUT_F32 | GBX_ACCUMULATE)) return GBA_ERR_SHAPE;
+    if ((flags & GBX_ACCUMULATE) && !(flags & GBX_OUT_F32)) return GBA_ERR_DTYPE;
+    if ((s = check_sizes(T, E, 0, N))) return s;
+    if ((s = check_sizes(T, E, 0, K))) return s;
+    if ((K % 8) || (N % 8)) return GBA_ERR_ALIGN;
+    const size_t ob = (flags & GBX_OUT_F32) ? 4 : 2;
+    const Span spans[] = {{A, size3(T, K, 2), true, false, 16},
+                          {dC, size3(T, N, 2), true, false, 16},
+                          {offsets, (size_t)(E + 1) * 4, N > 0, false, 4},
+                          {dW, size3(E, N * ob, K), true, true, 16},
+                          {dbias, size3(E, N, ob), false, true, 16},
+                          {workspace, workspace_bytes, false, true, 16}};
+    if ((s = check_spans(spans))) return s;
+    if (N == 0) return GBA_OK;
+    if ((s = check_device())) return s;
+    const bool f32 = (flags & GBX_OUT_F32) != 0, add = (flags & GBX_ACCUMULATE) != 0;
+    gbx::Group g = {};
+    g.offsets = offsets;
+    g.T = (int)T;
+    g.E = (int)E;
+    g.flags = (f32 ? gbx::GF_F32 : 0) | (add ? gbx::GF_ADD : 0);
+    g.splits = 1;
+    if (K > 0) {
+        // Rows of the output: the columns of the first factor (dC with GBA_TRANSPOSE_B).
+        const bool nk = (flags & GBA_TRANSPOSE_B) != 0;
+        g.A = (const uint16_t *)(nk ? dC : A);
+        g.B = (const uint16_t *)(nk ? A : dC);
+        g.M = (int)(nk ? N : K);
+        g.N = (int)(nk ? K : N);
+        g.C = dW;
+        const int64_t tiles = E * ((g.M + 127) / 128) * ((g.N + 127) / 128);
+        const int tile = tiles >= 256 ? gbx::TILE_128x128 : gbx::TILE_64x64;
+        if ((s = hip_result(gbx::wgrad_tn[dtype][tile](g, t_stream)))) return s;
+    }
+    if (dbias) {
+        g.A = (const uint16_t *)dC;
+        g.N = (int)N;
+        g.C = dbias;
+        return hip_result(gbx::launch_column_sums(g, dtype, t_stream));
+    }
+    return GBA_OK;
+}
+
+int mx4_quantize(const void *X, void *codes, void *scales, int64_t M, int64_t K, int dtype) {
+    int s = check_enums(GBA_ACT_NONE, dtype);
+    if (s) return s;
+    if (M < 0 || K < 0 || M > kMaxRows || K > kMaxWidth) return GBA_ERR_SHAPE;
+    if (K % 32) return GBA_ERR_ALIGN;
+    const Span spans[] = {{X, size3(M, K, 2), true, false, 16},
+                          {codes, size3(M, K / 2, 1), true, true, 16},
+                          {scales, size3(M, (K + 127) / 128, 4), true, true, 16}};
+    if ((s = check_spans(spans))) return s;
+    if (M == 0 || K == 0) return GBA_OK;
+    if ((s = check_device())) return s;
+    auto *const kernel = dtype == GBA_DTYPE_F16 ? gbx::mx4_quantize_kernel<0> : gbx::mx4_quantize_kernel<1>;
+    hipLaunchKernelGGL(kernel, gbx::mx4_grid((int)M, (int)K), dim3(256), 0, t_stream, (const uint16_t *)X,
+                       (uint32_t *)codes, (uint32_t *)scales, (int)M, (int)K);
+    return hip_result(hipGetLastError());
+}
+
+int mx4_dequantize(const void *codes, const void *scales, void *X, int64_t M, int64_t K,
+                   int dtype) {
+    int s = check_enums(GBA_ACT_NONE, dtype);
+    if (s) return s;
+    if (M < 0 || K < 0 || M > kMaxRows || K > kMaxWidth) return GBA_ERR_SHAPE;
+    if (K % 32) return GBA_ERR_ALIGN;
+    const Span spans[] = {{X, size3(M, K, 2), true, true, 16},
+                          {codes, size3(M, K / 2, 1), true, false, 16},
+                          {scales, size3(M, (K + 127) / 128, 4), true, false, 16}};
+    if ((s = check_spans(spans))) return s;
+    if (M == 0 || K == 0) return GBA_OK;
+    if ((s = check_device())) return s;
+    auto *const kernel = dtype == GBA_DTYPE_F16 ? gbx::mx4_dequantize_kernel<0> : gbx::mx4_dequantize_kernel<1>;
+    hipLaunchKernelGGL(kernel, gbx::mx4_grid((int)M, (int)K), dim3(256), 0, t_stream, (const uint32_t *)codes,
+                       (const uint32_t *)scales, (uint16_t *)X, (int)M, (int)K);
+    return hip_result(hipGetLastError());
+}
+
+// offsets null: dense (E == 1).
+static int mx4_common(const void *a_codes, const void *a_scales, const int32_t *offsets, bool grouped,
+                      const void *w_codes, const void *w_scales, const void *bias, void *C,
+                      int64_t T, int64_t E, int64_t N, int64_t K, int act, int dtype,
+                      void *workspace, size_t workspace_bytes) {
+    int s = check_enums(act, dtype);
+    if (s) return s;
+    if (K < 0 || K > 4 * kMaxDepth) return GBA_ERR_SHAPE;
+    if ((s = check_sizes(T, E, 0, N))) return s;
+    if ((K % 32) || (N % 8)) return GBA_ERR_ALIGN;
+    const int64_t planes = (K + 127) / 128;
+    const Span spans[] = {{a_codes, size3(T, K / 2, 1), true, false, 16},
+                          {a_scales, size3(T, planes, 4), true, false, 16},
+                          {offsets, (size_t)(E + 1) * 4, grouped && T > 0 && N > 0, false, 4},
+                          {w_codes, size3(E, N, K / 2), T > 0, false, 16},
+                          {w_scales, size3(E * N, planes, 4), T > 0, false, 16},
+                          {bias, size3(E, N, 2), false, false, 16},
+                          {C, size3(T, N, 2), true, true, 16},
+                          {workspace, workspace_bytes, false, true, 16}};
+    if ((s = check_spans(spans))) return s;
+    if (T == 0 || N == 0) return GBA_OK;
+    if ((s = check_device())) return s;
+    gbx::Group g = {};
+    g.A = (const uint16_t *)a_codes;
+    g.B = (const uint16_t *)w_codes;
+    g.sa = (const uint32_t *)a_scales;
+    g.sb = (const uint32_t *)w_scales;
+    g.offsets = grouped ? offsets : nullptr;
+    g.bias = (const uint16_t *)bias;
+    g.C = C;
+    g.T = (int)T;
+    g.E = (int)E;
+    g.N = (int)N;
+    g.K = (int)(K / 4);   // 16-bit words of four codes
+    g.act = act;
+    g.splits = 1;
+    return hip_result(gbx::mx4_nt[dtype][row_tile(T, E)](g, t_stream));
+}
+
+int gemm_bias_act_mx4(const void *a_codes, const void *a_scales, const void *w_codes,
+                      const void *w_scales, const void *bias, void *C, int64_t M, int64_t N,
+                      int64_t K, int act, int dtype, void *workspace, size_t workspace_bytes) {
+    return mx4_common(a_codes, a_scales, nullptr, false, w_codes, w_scales, bias, C, M, 1, N, K, act, dtype,
+                      workspace, workspace_bytes);
+}
+
+int grouped_gemm_bias_act_mx4(const void *a_codes, const void *a_scales, const int32_t *offsets,
+                              const void *w_codes, const void *w_scales, const void *bias, void *C,
+                              int64_t T, int64_t E, int64_t N, int64_t K, int act, int dtype,
+                              void *workspace, size_t workspace_bytes) {
+    return mx4_common(a_codes, a_scales, offsets, true, w_codes, w_scales, bias, C, T, E, N, K, act, dtype,
+                      workspace, workspace_bytes);
+}
+
+}  // extern "C"

@@ -1,0 +1,199 @@
+// What the kernels of libgba_experts share: the arguments of a grouped product,
+// the search for the expert and tile of a work unit, activation slopes, and the
+// microscaled 4-bit matrix instruction.
+#pragma once
+
+#include "gba_dma.hpp"
+#include "gemm_v3.hpp"   // mfma16x16x32, aswz, bswz
+
+namespace gbx {
+
+using namespace gba;
+
+// Operand types. MX4 rows are counted in 16-bit words of four codes: a row of K
+// values is K / 4 words, and a 64-word slice (128 bytes) is 256 values, so the
+// 4-bit kernels move the same bytes in the same tiles as the 16-bit ones; only
+// the matrix instruction and its scales differ.
+enum { OP_F16 = 0, OP_BF16 = 1, OP_MX4 = 2 };
+
+// What the kernel does with a tile's fp32 sums.
+enum {
+    EPI_ACT = 0,    // act(sum + bias), and the rounded sum + bias where asked for
+    EPI_SLOPE = 1,  // sum * act'(z)
+    EPI_GRAD = 2,   // the sum, rounded or fp32, or added to what is there
+    EPI_PART = 3    // fp32 partial sums of one split
+};
+
+// A grouped product. Rows mode (weight gradients: see wgrad below): the rows of expert e of A [T][K] times
+// B_e, giving rows of C [T][N]. wgrad: At_e^T.B_e over the rows of expert e, with
+// At [T][M] and B [T][N], giving C [E][M][N]. K counts 16-bit words.
+struct Group {
+    const uint16_t *A, *B;
+    const uint32_t *sa, *sb;     // MX4 scale planes of A and B, one dword a row
+    const int32_t *offsets;      // null: one expert, all T rows
+    const uint16_t *bias;        // [E][N] or null
+    const uint16_t *z;           // EPI_SLOPE: [T][N]
+    void *C;
+    uint16_t *zout;              // EPI_ACT: [T][N] or null
+    float *part;                 // EPI_PART: [splits][rows of C][N]
+    int T, E, M, N, K;
+    int act, flags, splits;
+    int row_bound;               // rows mode: most row tiles the grid was made for
+};
+enum { GF_F32 = 1, GF_ADD = 2 };   // EPI_GRAD: fp32 output, added to what is there
+
+__device__ __forceinline__ int clamp_row(int v, int T) { return min(max(v, 0), T); }
+
+// First row and row count of expert e (uniform e): offsets clamped to [0, T].
+__device__ __forceinline__ void expert_rows(const Group &g, int e, int &start, int &rows) {
+    if (!g.offsets) {
+        start = 0;
+        rows = g.T;
+        return;
+    }
+    start = clamp_row(g.offsets[e], g.T);
+    rows = max(clamp_row(g.offsets[e + 1], g.T) - start, 0);
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Row tiles of all experts (rows mode), each wave for itself: lane l takes
+// experts l, l + 64, ... Offsets that decrease can name more tiles than the
+// grid was made for; those are left out.
+__device__ __forceinline__ int total_row_tiles(const Group &g, int bm, int lane) {
+    long long n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int t = 0;
+        if (e0 + lane < g.E) {
+            int start, rows;
+            expert_rows(g, e0 + lane, start, rows);
+            t = ceil_div(rows, bm);
+        }
+        n += t;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) n += __shfl_xor(n, d);
+    return __builtin_amdgcn_readfirstlane((int)min(n, (long long)g.row_bound));
+}
+
+// The expert that row tile number t (in expert order, t < total_row_tiles) lies
+// in, with the number of row tiles before it, its tiles, rows and first row. Every lane gets
+// the same answer.
+struct Found {
+    int e, before, tiles, start, rows;
+};
+__device__ __forceinline__ Found find_row_tile(const Group &g, int bm, int t, int lane) {
+    Found f = {0, 0, 0, 0, 0};
+    int before = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int n = 0, start = 0, rows = 0;
+        if (e0 + lane < g.E) {
+            expert_rows(g, e0 + lane, start, rows);
+            n = ceil_div(rows, bm);
+        }
+        const int upto = wave_scan(n, lane);
+        const unsigned long long past = __ballot(before + upto > t);
+        if (past) {
+            const int l = __ffsll(past) - 1;
+            f.e = e0 + l;
+            f.tiles = __shfl(n, l);
+            f.before = before + __shfl(upto, l) - f.tiles;
+            f.start = __shfl(start, l);
+            f.rows = __shfl(rows, l);
+            break;
+        }
+        before += __shfl(upto, 63);
+    }
+    f.e = __builtin_amdgcn_readfirstlane(f.e);
+    f.before = __builtin_amdgcn_readfirstlane(f.before);
+    f.tiles = __builtin_amdgcn_readfirstlane(f.tiles);
+    f.start = __builtin_amdgcn_readfirstlane(f.start);
+    f.rows = __builtin_amdgcn_readfirstlane(f.rows);
+    return f;
+}
+
+// ------------------------------------------------------- activation slopes --
+
+// act'(z) in fp32. relu'(0) = 0; at z = +-inf the limit; NaN for NaN.
+//  sigmoid:   t / (1 + t)^2 with t = e^-|z| (no cancellation on either side).
+//  softplus:  the logistic of z.
+//  gelu:      Phi(z) + z phi(z); Phi as in act_fn (2^Q(|z|) is Phi(-|z|), within 8e-6 of it).
+//  gelu_tanh: z = tanh form; with s = 1 / (1 + e), e = e^(-2y),
+//             y = sqrt(2/pi) (z + c z^3): s + z s (1 - s) 2 y', and 1 - s = e s.
+//             Outside |z| = 10 the slope is 0 or 1 to 1e-30: z is clamped there,
+//             which keeps e finite.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if constexpr (ACT == ACT_RELU) {
+        return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    } else if constexpr (ACT == ACT_SIGMOID) {
+        const float t = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e);
+        const float r = __builtin_amdgcn_rcpf(1.0f + t);
+        return t * r * r;
+    } else if constexpr (ACT == ACT_SOFTPLUS) {
+        return act_fn<ACT_SIGMOID>(z);
+    } else if constexpr (ACT == ACT_GELU) {
+        const float az = fminf(fabsf(z), 30.0f);
+        float q = fmaf(az, -1.8348076764596044e-06f, 6.15982135059312e-05f);
+        q = fmaf(az, q, -0.0009305241401307285f);
+        q = fmaf(az, q, 0.008507887832820415f);
+        q = fmaf(az, q, -0.05396006256341934f);
+        q = fmaf(az, q, -0.4584644138813019f);
+        q = fmaf(az, q, -1.1512510776519775f);
+        q = fmaf(az, q, -0.9999952912330627f);
+        const float lower = __builtin_amdgcn_exp2f(q);   // Phi(-|z|)
+        // |z| phi(z), 1 / sqrt(2 pi) = 0.39894228
+        const float zp = az * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * az * az);
+        // z > 0: 1 - lower + zp; z < 0: lower - zp
+        const float d = zp - lower;
+        const float r = z > 0.0f ? 1.0f + d : -d;
+        return z != z ? z : r;
+    } else if constexpr (ACT == ACT_GELU_TANH) {
+        const float c = fminf(fmaxf(z, -10.0f), 10.0f);
+        const float c2 = c * c;
+        const float e = __builtin_amdgcn_exp2f(-c * fmaf(c2, 0.10294324159622192f, 2.302208185195923f));
+        const float s = __builtin_amdgcn_rcpf(1.0f + e);
+        // 2 y' = 2 sqrt(2/pi) (1 + 3 c z^2) = 1.5957691 + 0.21406545 z^2
+        const float r = fmaf(c * (e * s) * s, fmaf(c2, 0.21406544f, 1.5957691216057308f), s);
+        return z != z ? z : r;
+    } else {
+        return 1.0f;
+    }
+}
+
+// f(std::integral_constant<int, act>{}) for the run-time act (uniform).
+template <class F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
+    switch (act) {
+    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>{}); break;
+    case ACT_SIGMOID: f(std::integral_constant<int, ACT_SIGMOID>{}); break;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
+    case ACT_SOFTPLUS: f(std::integral_constant<int, ACT_SOFTPLUS>{}); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, ACT_NONE>{}); break;
+    }
+}
+
+// ------------------------------------------------------------------- MX4 ----
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// c + A.B on 16 x 16 x 128 blocks of 4-bit codes: lane l holds row / column l % 16
+// and the 32 codes of block l / 16 (16 bytes), and in the low byte of its scale
+// operand that block's exponent. Results lie as those of the 16-bit 16x16x32 instruction.
+__device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+    const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const i32x8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+}  // namespace gbx

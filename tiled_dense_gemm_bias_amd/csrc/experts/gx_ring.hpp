@@ -1,0 +1,314 @@
+// Tile kernel of the grouped products: one BM x BN tile of one expert's output
+// per workgroup, K walked in 64-word slices (128 bytes a row) through a ring of
+// LDS stages that direct-to-LDS loads fill STAGES - 1 slices ahead.
+//
+// A workgroup finds its expert itself: the row tiles of all experts are counted
+// from the offsets in device memory (a wave scan, redone by every wave), so the
+// host needs no copy of them. The grid is the most tiles T rows can make; the
+// workgroups past the last tile end at once.
+//
+// Operand layouts: K-contiguous rows (A; B with TB) and rows along K (B [K][N]
+// without TB; At [T][M] with TA), in LDS as in gemm_v3.hpp, chunks XOR-swizzled so that
+// the fragment reads have no bank conflicts. Edges cost no branches: rows past
+// the expert's end, columns past N and words past K read as zeros (buffer range
+// checks and out-of-range offsets).
+#pragma once
+
+#include "gx_common.hpp"
+
+namespace gbx {
+
+template <int BM, int BN, int WM, int WN, int STAGES, int OP, int ODT, int EPI, bool TB, bool TA>
+__global__ void __launch_bounds__(256)
+grouped_ring_kernel(Group g) {
+    constexpr int NT = 256, BK = 64;
+    constexpr bool MX = OP == OP_MX4;
+    constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
+    constexpr int CHT = BM / 8, CHB = BN / 8;   // chunks per k row of At's and B's tiles
+    constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    // MX4: a slice's scales, 2 planes of one dword a row for A, then for B
+    constexpr int S_BYTES = MX ? 8 * (BM + BN) : 0;
+    constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
+    // Loads of a slice per thread. A tile of fewer than 256 chunks is loaded
+    // by every group of waves that it fills, the same bytes to the same place.
+    constexpr int A_LD = BM * 8 >= NT ? BM * 8 / NT : 1, B_LD = BN * 8 / NT;
+    constexpr int AW = BM * 8 >= NT ? 4 : BM * 8 / 64;   // waves that a load of A fills
+    constexpr int LD = A_LD + B_LD + (MX ? 1 : 0);
+    static_assert(WM * WN == 4 && WTM % 16 == 0 && WTN % 16 == 0, "four waves of whole MFMA blocks");
+    static_assert(BN * 8 % NT == 0 && (BM * 8 % NT == 0 || NT % (BM * 8) == 0), "loads split evenly");
+    static_assert(!TA || (CHT >= 8 && !TB && !MX), "At: 64 rows or more");
+    static_assert(TB || CHB >= 8, "B swizzle needs 8 chunks per row");
+    static_assert(!MX || (TB && BM <= 256 && BN <= 256), "4-bit operands are K-contiguous");
+    static_assert(STAGES * STAGE <= 160 * 1024 && (STAGES - 1) * LD < 64, "ring");
+
+    __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wid / WN, wn = wid % WN;
+
+    // ---- the work unit: expert, tile, K range ----
+    const int tiles_n = ceil_div(g.N, BN);
+    int e, start, rows, m0, n0, split;
+    {
+        const int row_tiles = TA ? 0 : total_row_tiles(g, BM, lane);
+        const int tiles_m = ceil_div(g.M, BM);   // TA
+        const long long tiles = TA ? (long long)g.E * tiles_m * tiles_n : (long long)row_tiles * tiles_n;
+        const long long units = tiles * g.splits;
+        const long long b = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+        if (b >= units) return;
+        int u = xcd_remap((int)b, (int)units);
+        split = u / (int)tiles;
+        u -= split * (int)tiles;
+        int tm, tn;
+        if constexpr (TA) {
+            e = u / (tiles_m * tiles_n);
+            grouped_tile(u - e * tiles_m * tiles_n, tiles_m, tiles_n, 4, tm, tn);
+            expert_rows(g, e, start, rows);
+        } else {
+            const Found f = find_row_tile(g, BM, u / tiles_n, lane);
+            e = f.e;
+            start = f.start;
+            rows = f.rows;
+            grouped_tile(u - f.before * tiles_n, f.tiles, tiles_n, 4, tm, tn);
+        }
+        m0 = tm * BM;
+        n0 = tn * BN;
+    }
+    const int K = TA ? rows : g.K;          // depth of the sum
+    const int M = TA ? g.M : rows;          // rows of the expert's output
+    const int N = g.N;
+    const int nk_all = ceil_div(K, BK);
+    const int kt0 = (int)((long long)split * nk_all / g.splits);
+    const int nk = (int)((long long)(split + 1) * nk_all / g.splits) - kt0;
+    const int rows_a = min(M - m0, BM), rows_b = min(N - n0, BN);
+    const uint16_t *const Ae = g.A + (TA ? (size_t)start * M : (size_t)start * K);
+    const uint16_t *const Be = TA ? g.B + (size_t)start * N : g.B + (size_t)e * K * N;
+
+    // ---- loads ----
+    // Byte offsets from a slice's corner, which the descriptor carries. Load i of
+    // a K-contiguous tile: row i*32 + tid/8, chunk (tid%8) ^ (row%8); of a tile
+    // with rows along K: k row, chunk ^ bswz(k row), columns past the edge out of range.
+    uint32_t off[A_LD + B_LD];
+    const int ta = tid & (AW * 64 - 1);
+    const int ca = (tid & 7) ^ ((tid >> 3) & 7);   // chunk of every K-contiguous load
+#pragma unroll
+    for (int i = 0; i < A_LD; ++i) {
+        const int s = i * NT + ta;
+        if constexpr (TA) {
+            const int r = s / CHT, c = (s % CHT) ^ bswz<CHT>(r);
+            off[i] = m0 + c * 8 < M ? (uint32_t)r * (uint32_t)M * 2u + (uint32_t)c * 16u : kOobOffset;
+        } else {
+            off[i] = (uint32_t)(s >> 3) * (uint32_t)K * 2u + (uint32_t)ca * 16u;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < B_LD; ++i) {
+        const int s = i * NT + tid;
+        if constexpr (TB) {
+            off[A_LD + i] = (uint32_t)(s >> 3) * (uint32_t)K * 2u + (uint32_t)ca * 16u;
+        } else {
+            const int r = s / CHB, c = (s % CHB) ^ bswz<CHB>(r);
+            off[A_LD + i] = n0 + c * 8 < N ? (uint32_t)r * (uint32_t)N * 2u + (uint32_t)c * 16u : kOobOffset;
+        }
+    }
+    const uint32_t smem_lds = (uint32_t)(uintptr_t)(GBA_LDS void *)smem;
+    // Slice kt (of this unit) into stage `stage`; a slice past the last reads
+    // nothing and lands zeros, which keeps the wait counts uniform.
+    auto load_slice = [&](int kt, int stage) __attribute__((always_inline)) {
+        const bool live = kt < nk;
+        const int k0 = (kt0 + (live ? kt : 0)) * BK;
+        const uint32_t kin = live ? (uint32_t)min(K - k0, BK) : 0u;
+        const bool in_k = (uint32_t)ca * 8u < kin;   // K-contiguous tiles: chunk inside K
+        const uint32_t base = smem_lds + (uint32_t)(stage * STAGE);
+        const __amdgpu_buffer_rsrc_t ra =
+            TA ? make_rsrc(Ae + (size_t)k0 * M + m0, kin * (uint32_t)M * 2u)
+               : make_rsrc(Ae + (size_t)m0 * K + k0, live ? (uint32_t)rows_a * (uint32_t)K * 2u - (uint32_t)k0 * 2u : 0u);
+        const __amdgpu_buffer_rsrc_t rb =
+            TB ? make_rsrc(Be + (size_t)n0 * K + k0, live ? (uint32_t)rows_b * (uint32_t)K * 2u - (uint32_t)k0 * 2u : 0u)
+               : make_rsrc(Be + (size_t)k0 * N + n0, kin * (uint32_t)N * 2u);
+        const uint32_t wave_a = base + (uint32_t)((wid & (AW - 1)) * 1024);
+#pragma unroll
+        for (int i = 0; i < A_LD; ++i)
+            buffer_load_lds16(ra, TA || in_k ? off[i] : kOobOffset, wave_a + (uint32_t)(i * NT * 16));
+#pragma unroll
+        for (int i = 0; i < B_LD; ++i)
+            buffer_load_lds16(rb, !TB || in_k ? off[A_LD + i] : kOobOffset,
+                              base + (uint32_t)(A_BYTES + wid * 1024 + i * NT * 16));
+        if constexpr (MX) {
+            // Wave w loads plane w % 2 of A's (w < 2) or B's scales: four rows'
+            // dwords a lane (range checks are per dword), lanes past the tile nothing.
+            const int plane = 2 * (kt0 + kt) + (wid & 1);
+            const bool there = live && plane * 32 < K;   // 32 words: 128 values a plane
+            const bool of_a = wid < 2;
+            const size_t all = of_a ? (size_t)g.T : (size_t)g.E * N;
+            const uint32_t *const src = of_a ? g.sa + (size_t)start + m0 : g.sb + (size_t)e * N + n0;
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(src + (there ? (size_t)plane * all : 0),
+                                                        there ? (uint32_t)(of_a ? rows_a : rows_b) * 4u : 0u);
+            const int mine = of_a ? BM : BN;
+            const uint32_t dst = base + (uint32_t)(A_BYTES + B_BYTES) +
+                                 (of_a ? (uint32_t)((wid & 1) * BM * 4) : (uint32_t)(2 * BM * 4 + (wid & 1) * BN * 4));
+            // The lanes past the tile's rows write nowhere: they are switched off.
+            if (lane * 4 < mine) buffer_load_lds16(rs, (uint32_t)lane * 16u, dst);
+        }
+    };
+
+    // ---- fragments ----
+    const int tg = lane >> 4, tj = lane & 15;
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+        for (int b = 0; b < FM; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto compute = [&](int stage) __attribute__((always_inline)) {
+        const char *const base = smem + stage * STAGE;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 af[FM], bf[FN];
+            uint32_t saf[FM], sbf[FN];
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                if constexpr (TA) {
+                    i16x4 h[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = kk * 32 + 8 * tg + 4 * i + (tj >> 2);
+                        const int m = wm * WTM + f * 16 + 4 * (tj & 3);
+                        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (GBA_LDS i16x4 *)(base + k * (BM * 2) + (((m >> 3) ^ bswz<CHT>(k)) * 16) + (m & 4) * 2));
+                    }
+                    af[f] = __builtin_bit_cast(u32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                } else {
+                    const int r = wm * WTM + f * 16 + tj;
+                    af[f] = *reinterpret_cast<const u32x4 *>(base + r * 128 + (((4 * kk + tg) ^ (r & 7)) * 16));
+                }
+                if constexpr (MX)
+                    saf[f] = *reinterpret_cast<const uint32_t *>(base + A_BYTES + B_BYTES + kk * BM * 4 +
+                                                                 (wm * WTM + f * 16 + tj) * 4) >> (8 * tg);
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                if constexpr (TB) {
+                    const int r = wn * WTN + f * 16 + tj;
+                    bf[f] = *reinterpret_cast<const u32x4 *>(base + A_BYTES + r * 128 + (((4 * kk + tg) ^ (r & 7)) * 16));
+                } else {
+                    i16x4 h[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = kk * 32 + 8 * tg + 4 * i + (tj >> 2);
+                        const int n = wn * WTN + f * 16 + 4 * (tj & 3);
+                        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (GBA_LDS i16x4 *)(base + A_BYTES + k * (BN * 2) + (((n >> 3) ^ bswz<CHB>(k)) * 16) + (n & 4) * 2));
+                    }
+                    bf[f] = __builtin_bit_cast(u32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+                if constexpr (MX)
+                    sbf[f] = *reinterpret_cast<const uint32_t *>(base + A_BYTES + B_BYTES + 2 * BM * 4 + kk * BN * 4 +
+                                                                 (wn * WTN + f * 16 + tj) * 4) >> (8 * tg);
+            }
+#pragma unroll
+            for (int a = 0; a < FN; ++a)
+#pragma unroll
+                for (int b = 0; b < FM; ++b) {
+                    if constexpr (MX)
+                        acc[a][b] = mfma_mx4(bf[a], af[b], acc[a][b], sbf[a], saf[b]);
+                    else
+                        acc[a][b] = mfma16x16x32<OP>(bf[a], af[b], acc[a][b]);
+                }
+        }
+    };
+
+    // ---- the slices ----
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) load_slice(s, s);
+    int stage = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        // Slice kt has landed and this wave's reads of slice kt - 1 are done; then
+        // the same holds for all waves, and slice kt - 1's stage is free.
+        wait_vmcnt_lgkm0<(STAGES - 2) * LD>();
+        block_barrier();
+        load_slice(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+        compute(stage);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    wait_vmcnt<0>();   // no direct-to-LDS write may outlive the workgroup's LDS
+
+    // ---- epilogue: lane l holds row l % 16, columns 4 (l / 16) .. +3 of each block ----
+    const size_t crow = TA ? (size_t)e * M : (size_t)start;
+    auto each_block = [&](auto &&f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < FN; ++a) {
+            const int n = n0 + wn * WTN + a * 16 + 4 * tg;
+            if (n >= N) continue;
+#pragma unroll
+            for (int b = 0; b < FM; ++b) {
+                const int m = m0 + wm * WTM + b * 16 + tj;
+                if (m >= M) continue;
+                f(acc[a][b], n, (crow + m) * (size_t)N + n);
+            }
+        }
+    };
+    auto four = [](const uint16_t *p) __attribute__((always_inline)) {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+        return f32x4{to_f32<ODT>(v.x & 0xffffu), to_f32<ODT>(v.x >> 16), to_f32<ODT>(v.y & 0xffffu), to_f32<ODT>(v.y >> 16)};
+    };
+    auto store4 = [](uint16_t *p, const f32x4 &v) __attribute__((always_inline)) {
+        *reinterpret_cast<u32x2 *>(p) = u32x2{pack2<ODT>(v[0], v[1]), pack2<ODT>(v[2], v[3])};
+    };
+    if constexpr (EPI == EPI_PART) {
+        float *const P = g.part + (size_t)split * (TA ? (size_t)g.E * M : (size_t)g.T) * N;
+        each_block([&](const f32x4 &a, int, size_t at) { *reinterpret_cast<f32x4 *>(P + at) = a; });
+    } else if constexpr (EPI == EPI_ACT) {
+        const uint16_t *const bias = g.bias ? g.bias + (size_t)e * N : nullptr;
+        with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act_c)::value;
+            each_block([&](f32x4 a, int n, size_t at) {
+                if (bias) a += four(bias + n);
+                if (g.zout) store4(g.zout + at, a);
+                store4((uint16_t *)g.C + at, f32x4{act_fn<ACT>(a[0]), act_fn<ACT>(a[1]), act_fn<ACT>(a[2]), act_fn<ACT>(a[3])});
+            });
+        });
+    } else if constexpr (EPI == EPI_SLOPE) {
+        with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act_c)::value;
+            each_block([&](f32x4 a, int, size_t at) {
+                if constexpr (ACT != ACT_NONE) {
+                    const f32x4 z = four(g.z + at);
+                    a *= f32x4{act_slope<ACT>(z[0]), act_slope<ACT>(z[1]), act_slope<ACT>(z[2]), act_slope<ACT>(z[3])};
+                }
+                store4((uint16_t *)g.C + at, a);
+            });
+        });
+    } else {
+        if (g.flags & GF_F32) {
+            each_block([&](f32x4 a, int, size_t at) {
+                f32x4 *const p = reinterpret_cast<f32x4 *>((float *)g.C + at);
+                *p = (g.flags & GF_ADD) ? a + *p : a;
+            });
+        } else {
+            each_block([&](const f32x4 &a, int, size_t at) { store4((uint16_t *)g.C + at, a); });
+        }
+    }
+}
+
+// Most row tiles that T rows of E experts can make: one for each full tile, and
+// one more for each expert that has rows.
+inline long long row_tile_bound(long long T, long long E, int bm) {
+    return T / bm + (E < T ? E : T);
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int OP, int ODT, int EPI, bool TB, bool TA>
+hipError_t launch_ring(Group g, hipStream_t stream) {
+    const long long tiles_n = ceil_div(g.N, BN);
+    const long long row_tiles = TA ? (long long)g.E * ceil_div(g.M, BM) : row_tile_bound(g.T, g.E, BM);
+    const long long units = row_tiles * tiles_n * g.splits;
+    if (units <= 0) return hipSuccess;
+    if (units > 0x7fffffffLL - kGridX) return hipErrorInvalidValue;
+    g.row_bound = (int)row_tiles;
+    hipLaunchKernelGGL((grouped_ring_kernel<BM, BN, WM, WN, STAGES, OP, ODT, EPI, TB, TA>), tile_grid(units),
+                       dim3(256), 0, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace gbx

@@ -1,0 +1,283 @@
+"""Python binding of libgba_experts: products grouped by expert, forward and
+backward, and microscaled 4-bit floating point (see include/gba_experts.h for the
+C ABI). The names here are also names of the package.
+
+Rows are sorted by expert: rows offsets[e] .. offsets[e+1] - 1 belong to expert
+e, with offsets an int32 device tensor of E + 1 entries that the host never reads.
+
+    gba.grouped_gemm_bias_act(a, offsets, w, bias, h, "gelu", transpose_b=True, preact=z)
+    gba.grouped_gemm_act_grad(dy, offsets, w2, z, dz, "gelu", transpose_b=True)
+    gba.grouped_gemm_wgrad(a, dz, offsets, dw, db, transpose_b=True)
+
+As in the rest of the package the caller owns every tensor, work runs on the
+current stream, and tensors used on another stream than the one they were made
+on are the caller's to keep alive (torch's record_stream).
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+from . import GbaError, TRANSPOSE_B, _act, _check_dev, _dtype_code, _torch, _ws_args
+
+_HERE = os.path.dirname(os.path.abspath(__file__))
+EXPERTS_LIB_PATH = os.path.join(_HERE, "libgba_experts.so")
+EXPERTS_HEADER = os.path.join(os.path.dirname(_HERE), "include", "gba_experts.h")
+
+OUT_F32 = 16
+ACCUMULATE = 32
+
+_LIB = None
+
+
+def _lib():
+    global _LIB
+    if _LIB is None:
+        if not os.path.exists(EXPERTS_LIB_PATH):
+            raise ImportError("libgba_experts.so is not built; run: python -m tiled_dense_gemm_bias_amd.build")
+        lib = ctypes.CDLL(EXPERTS_LIB_PATH)
+        p, i64, ci, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        sig = {
+            "grouped_gemm_bias_act": [p] * 6 + [i64] * 4 + [ci, ci, ci, p, sz],
+            "grouped_gemm_act_grad": [p] * 5 + [i64] * 4 + [ci, ci, ci, p, sz],
+            "grouped_gemm_wgrad": [p] * 5 + [i64] * 4 + [ci, ci, p, sz],
+            "mx4_quantize": [p, p, p, i64, i64, ci],
+            "mx4_dequantize": [p, p, p, i64, i64, ci],
+            "gemm_bias_act_mx4": [p] * 6 + [i64] * 3 + [ci, ci, p, sz],
+            "grouped_gemm_bias_act_mx4": [p] * 7 + [i64] * 4 + [ci, ci, p, sz],
+            "gbx_set_stream": [p],
+            "gbx_last_hip_error": [],
+            "gbx_version": [],
+        }
+        for name, args in sig.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = ci
+        lib.gbx_version.restype = ctypes.c_char_p
+        _LIB = lib
+    return _LIB
+
+
+def experts_lib():
+    """The raw ctypes handle of libgba_experts.so (C ABI of include/gba_experts.h)."""
+    return _lib()
+
+
+def experts_version() -> str:
+    return _lib().gbx_version().decode()
+
+
+def _call(fn_name, dev, *args):
+    """Run entry point fn_name on dev's current stream (see the package's _call)."""
+    torch = _torch()
+    lib = _LIB or _lib()
+    C = torch._C
+    if dev.index == C._cuda_getDevice():
+        lib.gbx_set_stream(C._cuda_getCurrentRawStream(dev.index))
+        st = getattr(lib, fn_name)(*args)
+    else:
+        with torch.cuda.device(dev):
+            lib.gbx_set_stream(C._cuda_getCurrentRawStream(dev.index))
+            st = getattr(lib, fn_name)(*args)
+    if st != 0:
+        raise GbaError(st, fn_name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    _check_dev(workspace)
+    return _ws_args(workspace)
+
+
+def _offsets(offsets, E):
+    if offsets.dtype != _torch().int32:
+        raise TypeError("offsets are int32, got %s" % offsets.dtype)
+    if tuple(offsets.shape) != (E + 1,):
+        raise ValueError("offsets has E + 1 = %d entries, got shape %s" % (E + 1, tuple(offsets.shape)))
+
+
+def _same_dtype(first, *rest):
+    dt = _dtype_code(first)
+    for t in rest:
+        if t is not None and t.dtype != first.dtype:
+            raise TypeError("all operands must share one dtype")
+    return dt
+
+
+def _expect(what, t, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError("shape mismatch: %s is %s, expected %s" % (what, tuple(t.shape), shape))
+
+
+def grouped_gemm_bias_act(a, offsets, w, bias, c, act="gelu", transpose_b=False, preact=None,
+                          workspace=None):
+    """c[r] = act(a[r] @ w[e] + bias[e]) for the rows r of each expert e. Returns c.
+
+    a [T,K]; offsets int32 [E+1]; w [E,K,N], or [E,N,K] with transpose_b; bias
+    [E,N] or None; c [T,N]. preact: [T,N] or None, receives a[r] @ w[e] + bias[e]
+    rounded (grouped_gemm_act_grad's z). Rows of no expert are not written.
+    workspace: optional device tensor (a few MiB) that lets calls with few output
+    tiles split K."""
+    dev = _check_dev(a, offsets, w, bias, c, preact)
+    dt = _same_dtype(a, w, bias, c, preact)
+    T, K = a.shape
+    E, N = w.shape[0], w.shape[1 if transpose_b else 2]
+    _expect("w", w, (E, N, K) if transpose_b else (E, K, N))
+    _expect("c", c, (T, N))
+    _expect("bias", bias, (E, N))
+    _expect("preact", preact, (T, N))
+    _offsets(offsets, E)
+    ws, nb = _workspace(workspace)
+    _call("grouped_gemm_bias_act", dev, _addr(a), _addr(offsets), _addr(w), _addr(bias), _addr(c),
+          _addr(preact), T, E, N, K, _act(act), dt, TRANSPOSE_B if transpose_b else 0, ws, nb)
+    return c
+
+
+def grouped_gemm_act_grad(dc, offsets, w, z, da, act="gelu", transpose_b=False, workspace=None):
+    """da[r] = (dc[r] @ w[e].T) * act'(z[r]): the input gradient of
+    grouped_gemm_bias_act, carried through the activation that made its input
+    (a = act(z)). Returns da.
+
+    w and transpose_b as in the forward call; dc [T,N]; z, da [T,K]. act "none":
+    da = dc @ w[e].T, and z may be None."""
+    dev = _check_dev(dc, offsets, w, z, da)
+    dt = _same_dtype(dc, w, z, da)
+    T, N = dc.shape
+    E, K = w.shape[0], w.shape[2 if transpose_b else 1]
+    _expect("w", w, (E, N, K) if transpose_b else (E, K, N))
+    _expect("da", da, (T, K))
+    _expect("z", z, (T, K))
+    _offsets(offsets, E)
+    ws, nb = _workspace(workspace)
+    _call("grouped_gemm_act_grad", dev, _addr(dc), _addr(offsets), _addr(w), _addr(z), _addr(da),
+          T, E, N, K, _act(act), dt, TRANSPOSE_B if transpose_b else 0, ws, nb)
+    return da
+
+
+def grouped_gemm_wgrad(a, dc, offsets, dw, dbias=None, accumulate=False, transpose_b=False,
+                       workspace=None):
+    """dw[e] = a_e.T @ dc_e ([E,K,N]), or dc_e.T @ a_e ([E,N,K]) with transpose_b:
+    the layout w has in the forward call; dbias[e] = dc_e.sum(0). Returns dw.
+
+    a [T,K], dc [T,N], of one 16-bit dtype; dw and dbias of that dtype or both
+    float32. accumulate (float32 only): added to what they hold. An empty expert's
+    gradients are zero."""
+    torch = _torch()
+    dev = _check_dev(a, dc, offsets, dw, dbias)
+    dt = _same_dtype(a, dc)
+    T, K = a.shape
+    N, E = dc.shape[1], dw.shape[0]
+    _expect("dc", dc, (T, N))
+    _expect("dw", dw, (E, N, K) if transpose_b else (E, K, N))
+    _expect("dbias", dbias, (E, N))
+    _offsets(offsets, E)
+    flags = TRANSPOSE_B if transpose_b else 0
+    if dw.dtype == torch.float32:
+        flags |= OUT_F32
+    elif dw.dtype != a.dtype:
+        raise TypeError("dw has the operands' dtype or float32")
+    if dbias is not None and dbias.dtype != dw.dtype:
+        raise TypeError("dbias has dw's dtype")
+    if accumulate:
+        if dw.dtype != torch.float32:
+            raise TypeError("accumulate needs float32 gradients")
+        flags |= ACCUMULATE
+    ws, nb = _workspace(workspace)
+    _call("grouped_gemm_wgrad", dev, _addr(a), _addr(dc), _addr(offsets), _addr(dw), _addr(dbias),
+          T, E, N, K, dt, flags, ws, nb)
+    return dw
+
+
+def mx4_scales_shape(M: int, K: int) -> tuple:
+    """Shape of the scale planes of an [M,K] matrix: [ceil(K/128), M, 4]."""
+    return (-(-K // 128), M, 4)
+
+
+def mx4_pack_scales(rows):
+    """Scale planes of scale bytes given by rows ([M, K/32] uint8, the layout of the
+    OCP MX specification's blocks in row order)."""
+    torch = _torch()
+    M, blocks = rows.shape
+    planes = -(-blocks // 4)
+    full = torch.zeros(M, planes * 4, dtype=torch.uint8, device=rows.device)
+    full[:, :blocks] = rows
+    return full.view(M, planes, 4).transpose(0, 1).contiguous()
+
+
+def mx4_unpack_scales(scales, K: int):
+    """Scale bytes by rows ([M, K/32]) of scale planes."""
+    return scales.transpose(0, 1).reshape(scales.shape[1], -1)[:, :K // 32].contiguous()
+
+
+def _mx4(what, codes, scales, M, K):
+    torch = _torch()
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError("4-bit codes and scales are uint8 tensors")
+    if K % 32:
+        raise ValueError("%s: K must be a multiple of 32, got %d" % (what, K))
+    if codes.numel() != M * K // 2:
+        raise ValueError("%s: %d rows of %d codes are %d bytes, got shape %s" % (what, M, K, M * K // 2,
+                                                                                 tuple(codes.shape)))
+    _expect(what + " scales", scales, (-(-K // 128), M, 4))
+
+
+def mx4_quantize(x, codes, scales):
+    """Quantise x [M,K] (float16 or bfloat16, K a multiple of 32) to microscaled 4-bit
+    floats: codes uint8 [M,K/2], scales uint8 [ceil(K/128),M,4]. Returns (codes, scales)."""
+    dev = _check_dev(x, codes, scales)
+    M, K = x.shape
+    _mx4("codes", codes, scales, M, K)
+    _call("mx4_quantize", dev, _addr(x), _addr(codes), _addr(scales), M, K, _dtype_code(x))
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, x):
+    """x [M,K] (float16 or bfloat16) = the values of codes and scales. Returns x."""
+    dev = _check_dev(codes, scales, x)
+    M, K = x.shape
+    _mx4("codes", codes, scales, M, K)
+    _call("mx4_dequantize", dev, _addr(codes), _addr(scales), _addr(x), M, K, _dtype_code(x))
+    return x
+
+
+def gemm_bias_act_mx4(a_codes, a_scales, w_codes, w_scales, bias, c, act="gelu", workspace=None):
+    """c[M,N] = act(a @ w.T + bias) with a [M,K] and w [N,K] as mx4_quantize leaves
+    them; bias [N] or None and c float16 or bfloat16. Returns c."""
+    dev = _check_dev(a_codes, a_scales, w_codes, w_scales, bias, c)
+    dt = _same_dtype(c, bias)
+    (M, half), N = a_codes.shape, c.shape[1]
+    K = 2 * half
+    _expect("c", c, (M, N))
+    _expect("w_codes", w_codes, (N, half))
+    _expect("bias", bias, (N,))
+    _mx4("a", a_codes, a_scales, M, K)
+    _mx4("w", w_codes, w_scales, N, K)
+    ws, nb = _workspace(workspace)
+    _call("gemm_bias_act_mx4", dev, _addr(a_codes), _addr(a_scales), _addr(w_codes), _addr(w_scales),
+          _addr(bias), _addr(c), M, N, K, _act(act), dt, ws, nb)
+    return c
+
+
+def grouped_gemm_bias_act_mx4(a_codes, a_scales, offsets, w_codes, w_scales, bias, c, act="gelu",
+                              workspace=None):
+    """gemm_bias_act_mx4 by expert: a [T,K] sorted by expert, w_codes [E,N,K/2] with the
+    scale planes of the [E*N,K] matrix, bias [E,N] or None. Returns c."""
+    dev = _check_dev(a_codes, a_scales, offsets, w_codes, w_scales, bias, c)
+    dt = _same_dtype(c, bias)
+    (T, half), (E, N, _) = a_codes.shape, w_codes.shape
+    K = 2 * half
+    _expect("c", c, (T, N))
+    _expect("w_codes", w_codes, (E, N, half))
+    _expect("bias", bias, (E, N))
+    _mx4("a", a_codes, a_scales, T, K)
+    _mx4("w", w_codes, w_scales, E * N, K)
+    _offsets(offsets, E)
+    ws, nb = _workspace(workspace)
+    _call("grouped_gemm_bias_act_mx4", dev, _addr(a_codes), _addr(a_scales), _addr(offsets),
+          _addr(w_codes), _addr(w_scales), _addr(bias), _addr(c), T, E, N, K, _act(act), dt, ws, nb)
+    return c
