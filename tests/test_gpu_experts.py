@@ -61,6 +61,23 @@ SHAPES = [
 ]
 
 
+# Sizes that the 256 x 256 persistent kernels take (many row tiles, wide outputs),
+# with row, column and depth edges, empty experts, more experts than lanes, one tile more than a round.
+BIG = [
+    ([257, 0, 511, 300, 1000], 0, 0, 8200, 72),
+    ([513, 255], 3, 7, 12296, 200),
+    ([1, 700, 0, 0, 900], 0, 0, 8192, 128),
+    ([200] * 70, 0, 0, 1032, 136),
+    ([4096], 1, 0, 3080, 264),
+    ([300, 2000, 1, 0, 1000, 640], 0, 2, 4104, 1000),
+]
+BIG_GRAD = [
+    ([257, 0, 511, 1, 64], 0, 0, 2056, 1544),
+    ([65, 1000, 63, 300], 2, 5, 1800, 2048),
+    ([2000], 0, 0, 4104, 3080),
+]
+
+
 def build(seed, sizes, lead, tail, dtype):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return g, make_offsets(sizes, lead), lead + sum(sizes) + tail, len(sizes)
@@ -68,11 +85,11 @@ def build(seed, sizes, lead, tail, dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("tb", [True, False])
-@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("i", range(len(SHAPES + BIG)))
 def test_forward(i, tb, dtype):
-    sizes, lead, tail, N, K = SHAPES[i]
+    sizes, lead, tail, N, K = (SHAPES + BIG)[i]
     dt, act = DT[dtype], orc.ACTS[(i + tb) % 6]
-    say("forward", SHAPES[i], tb, dtype, act)
+    say("forward", i, sizes[:8], N, K, tb, dtype, act)
     g, off, T, E = build(100 + i, sizes, lead, tail, dt)
     a = draw(g, (T, K), dt)
     w = draw(g, (E, N, K) if tb else (E, K, N), dt, K ** -0.5)
@@ -98,11 +115,11 @@ def test_forward(i, tb, dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("tb", [True, False])
-@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("i", range(len(SHAPES + BIG)))
 def test_act_grad(i, tb, dtype):
-    sizes, lead, tail, K, N = SHAPES[i]
+    sizes, lead, tail, K, N = (SHAPES + BIG)[i]
     dt, act = DT[dtype], orc.ACTS[(i + 2 * tb) % 6]
-    say("act_grad", SHAPES[i], tb, dtype, act)
+    say("act_grad", i, sizes[:8], N, K, tb, dtype, act)
     g, off, T, E = build(200 + i, sizes, lead, tail, dt)
     dc = draw(g, (T, N), dt)
     w = draw(g, (E, N, K) if tb else (E, K, N), dt, N ** -0.5)
@@ -122,11 +139,11 @@ def test_act_grad(i, tb, dtype):
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("tb", [True, False])
 @pytest.mark.parametrize("out", ["own", "f32", "add"])
-@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("i", range(len(SHAPES + BIG_GRAD)))
 def test_wgrad(i, out, tb, dtype):
-    sizes, lead, tail, N, K = SHAPES[i]
+    sizes, lead, tail, N, K = (SHAPES + BIG_GRAD)[i]
     dt = DT[dtype]
-    say("wgrad", SHAPES[i], out, tb, dtype)
+    say("wgrad", i, sizes[:8], N, K, out, tb, dtype)
     g, off, T, E = build(300 + i, sizes, lead, tail, dt)
     a, dc = draw(g, (T, K), dt), draw(g, (T, N), dt)
     odt = dt if out == "own" else torch.float32

@@ -87,7 +87,8 @@ def test_quantise_every_value(dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 8, 32), (1, 1000, 4096), (5, 264, 96), (16, 64, 256), (17, 72, 288), (63, 136, 544),
-                                   (65, 200, 1024), (129, 264, 160), (300, 520, 2080), (513, 1032, 128)])
+                                   (65, 200, 1024), (129, 264, 160), (300, 520, 2080), (513, 1032, 128),
+                                   (1025, 10248, 288), (3000, 5128, 544), (4096, 4096, 512), (8200, 2056, 1312)])
 def test_product(M, N, K, dtype):
     dt, act = DT[dtype], orc.ACTS[(M + N) % 6]
     say("mx4 product", M, N, K, dtype, act)
@@ -109,7 +110,8 @@ def test_product(M, N, K, dtype):
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("sizes,lead,tail,N,K", [
     ([1], 0, 0, 8, 32), ([0, 3, 0, 1], 1, 0, 72, 160), ([5, 0, 16, 17], 0, 3, 136, 96), ([63, 0, 65, 2], 2, 1, 200, 544),
-    ([129, 255, 0, 130], 0, 5, 264, 288), ([1] * 70 + [0] * 20 + [3] * 20, 0, 0, 40, 128)])
+    ([129, 255, 0, 130], 0, 5, 264, 288), ([1] * 70 + [0] * 20 + [3] * 20, 0, 0, 40, 128),
+    ([257, 0, 511, 300, 1000], 0, 0, 8200, 288), ([200] * 70, 0, 3, 1032, 544), ([300, 2000, 1, 0, 1000, 640], 5, 0, 4104, 1056)])
 def test_grouped_product(sizes, lead, tail, N, K, dtype):
     dt, act = DT[dtype], orc.ACTS[len(sizes) % 6]
     say("mx4 grouped", sizes[:8], lead, tail, N, K, dtype, act)

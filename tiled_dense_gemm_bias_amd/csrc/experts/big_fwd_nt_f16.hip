@@ -1,0 +1,3 @@
+#include "gx_launch.hpp"
+
+GBX_BIG_TABLE(big_fwd_nt_f16, 0, 0, EPI_ACT, true)

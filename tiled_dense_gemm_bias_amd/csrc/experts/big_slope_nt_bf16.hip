@@ -1,0 +1,3 @@
+#include "gx_launch.hpp"
+
+GBX_BIG_TABLE(big_slope_nt_bf16, 1, 1, EPI_SLOPE, true)

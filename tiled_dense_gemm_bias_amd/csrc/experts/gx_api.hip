@@ -93,6 +93,13 @@ int check_sizes(int64_t T, int64_t E, int64_t depth, int64_t width) {
 
 size_t size3(int64_t a, int64_t b, int64_t c) { return (size_t)a * (size_t)b * (size_t)c; }
 
+// Whether 256 x 256 tiles (persistent kernel) fill the chip: rows of about
+// T / E an expert, `cols` columns, `slices` K slices.
+bool big_rows(int64_t T, int64_t E, int64_t cols, int64_t words) {
+    const int64_t some = E < T ? E : T, mean = T / some;
+    return words > 64 && mean >= 160 && (T / 256 + some / 2) * ((cols + 255) / 256) >= 192;
+}
+
 // Tile for rows of about T / E an expert.
 int row_tile(int64_t T, int64_t E) {
     const int64_t mean = T / (E < T ? E : T);
@@ -141,7 +148,13 @@ int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, 
     g.K = (int)K;
     g.act = act;
     g.splits = 1;
-    return hip_result(((flags & GBA_TRANSPOSE_B) ? gbx::fwd_nt : gbx::fwd_nn)[dtype][row_tile(T, E)](g, t_stream));
+    const bool nt = (flags & GBA_TRANSPOSE_B) != 0;
+    if (big_rows(T, E, N, K)) {
+        const gbx::LaunchFn *const big[2][2] = {{gbx::big_fwd_nn_f16, gbx::big_fwd_nn_bf16},
+                                                {gbx::big_fwd_nt_f16, gbx::big_fwd_nt_bf16}};
+        return hip_result(big[nt][dtype][act](g, t_stream));
+    }
+    return hip_result((nt ? gbx::fwd_nt : gbx::fwd_nn)[dtype][row_tile(T, E)](g, t_stream));
 }
 
 int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W, const void *z,
@@ -174,7 +187,13 @@ int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W,
     g.act = act;
     g.splits = 1;
     // W [E,N,K] has its rows along the sum, W [E,K,N] its columns.
-    return hip_result(((flags & GBA_TRANSPOSE_B) ? gbx::slope_nn : gbx::slope_nt)[dtype][row_tile(T, E)](g, t_stream));
+    const bool nt = !(flags & GBA_TRANSPOSE_B);
+    if (big_rows(T, E, K, N)) {
+        const gbx::LaunchFn *const big[2][2] = {{gbx::big_slope_nn_f16, gbx::big_slope_nn_bf16},
+                                                {gbx::big_slope_nt_f16, gbx::big_slope_nt_bf16}};
+        return hip_result(big[nt][dtype][act](g, t_stream));
+    }
+    return hip_result((nt ? gbx::slope_nt : gbx::slope_nn)[dtype][row_tile(T, E)](g, t_stream));
 }
 
 int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, void *dW,
@@ -214,7 +233,9 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
         g.C = dW;
         const int64_t tiles = E * ((g.M + 127) / 128) * ((g.N + 127) / 128);
         const int tile = tiles >= 256 ? gbx::TILE_128x128 : gbx::TILE_64x64;
-        if ((s = hip_result(gbx::wgrad_tn[dtype][tile](g, t_stream)))) return s;
+        const bool big = E * ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 192 && T / E >= 128;
+        s = hip_result(big ? gbx::big_wgrad_tn[dtype][f32](g, t_stream) : gbx::wgrad_tn[dtype][tile](g, t_stream));
+        if (s) return s;
     }
     if (dbias) {
         g.A = (const uint16_t *)dC;
@@ -296,6 +317,8 @@ static int mx4_common(const void *a_codes, const void *a_scales, const int32_t *
     g.K = (int)(K / 4);   // 16-bit words of four codes
     g.act = act;
     g.splits = 1;
+    if (big_rows(T, E, N, K / 4))
+        return hip_result((dtype == GBA_DTYPE_F16 ? gbx::big_mx4_f16 : gbx::big_mx4_bf16)[act](g, t_stream));
     return hip_result(gbx::mx4_nt[dtype][row_tile(T, E)](g, t_stream));
 }
 

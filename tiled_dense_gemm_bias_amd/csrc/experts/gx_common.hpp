@@ -44,7 +44,7 @@ enum { GF_F32 = 1, GF_ADD = 2 };   // EPI_GRAD: fp32 output, added to what is th
 
 __device__ __forceinline__ int clamp_row(int v, int T) { return min(max(v, 0), T); }
 
-// First row and row count of expert e (uniform e): offsets clamped to [0, T].
+// First row and row count of expert e: offsets clamped to [0, T].
 __device__ __forceinline__ void expert_rows(const Group &g, int e, int &start, int &rows) {
     if (!g.offsets) {
         start = 0;
@@ -53,6 +53,20 @@ __device__ __forceinline__ void expert_rows(const Group &g, int e, int &start, i
     }
     start = clamp_row(g.offsets[e], g.T);
     rows = max(clamp_row(g.offsets[e + 1], g.T) - start, 0);
+}
+
+// The same for a uniform e, into scalar registers by scalar loads (no kernel
+// writes the offsets), which wait for no vector memory.
+__device__ __forceinline__ void expert_rows_uniform(const Group &g, int e, int &start, int &rows) {
+    int lo = 0, hi = g.T;
+    if (g.offsets) {
+        typedef const int32_t __attribute__((address_space(4))) *ScalarPtr;
+        const ScalarPtr o = (ScalarPtr)(uintptr_t)g.offsets;
+        lo = o[e];
+        hi = o[e + 1];
+    }
+    start = __builtin_amdgcn_readfirstlane(clamp_row(lo, g.T));
+    rows = __builtin_amdgcn_readfirstlane(max(clamp_row(hi, g.T) - start, 0));
 }
 
 // Inclusive sum over the lanes of a wave.
@@ -82,6 +96,12 @@ __device__ __forceinline__ int total_row_tiles(const Group &g, int bm, int lane)
 #pragma unroll
     for (int d = 32; d > 0; d /= 2) n += __shfl_xor(n, d);
     return __builtin_amdgcn_readfirstlane((int)min(n, (long long)g.row_bound));
+}
+
+// Most row tiles that T rows of E experts can make: one for each full tile, and
+// one more for each expert that has rows.
+inline long long row_tile_bound(long long T, long long E, int bm) {
+    return T / bm + (E < T ? E : T);
 }
 
 // The expert that row tile number t (in expert order, t < total_row_tiles) lies

@@ -292,12 +292,6 @@ grouped_ring_kernel(Group g) {
     }
 }
 
-// Most row tiles that T rows of E experts can make: one for each full tile, and
-// one more for each expert that has rows.
-inline long long row_tile_bound(long long T, long long E, int bm) {
-    return T / bm + (E < T ? E : T);
-}
-
 template <int BM, int BN, int WM, int WN, int STAGES, int OP, int ODT, int EPI, bool TB, bool TA>
 hipError_t launch_ring(Group g, hipStream_t stream) {
     const long long tiles_n = ceil_div(g.N, BN);
