@@ -590,10 +590,18 @@ def cache_store(arch, cus, M, N, K, sched: dict, ms: float, act="gelu", dtype="f
     return st
 
 
-# Products grouped by expert and 4-bit floats (libgba_experts.so, loaded at the
-# first call).
-from .experts import (  # noqa: E402,F401
-    gemm_bias_act_mx4, grouped_gemm_act_grad, grouped_gemm_bias_act, grouped_gemm_bias_act_mx4,
-    grouped_gemm_wgrad, mx4_dequantize, mx4_pack_scales, mx4_quantize, mx4_scales_shape,
-    mx4_unpack_scales,
-)
+# Products grouped by expert and 4-bit floats: experts.py (libgba_experts.so and
+# torch are loaded when one of these names is first used).
+_EXPERTS = ("gemm_bias_act_mx4", "grouped_gemm_act_grad", "grouped_gemm_bias_act",
+            "grouped_gemm_bias_act_mx4", "grouped_gemm_wgrad", "mx4_dequantize", "mx4_pack_scales",
+            "mx4_quantize", "mx4_scales_shape", "mx4_unpack_scales")
+
+
+def __getattr__(name):
+    if name == "experts" or name in _EXPERTS:
+        import importlib
+        module = importlib.import_module(__name__ + ".experts")
+        for n in _EXPERTS:
+            globals()[n] = getattr(module, n)
+        return globals().get(name, module)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

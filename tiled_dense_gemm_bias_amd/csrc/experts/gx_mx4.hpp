@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t to_codes(uint32_t into, uint32_t two, float 
 
 // A wave takes 4 rows x 128 values, 16 lanes of 8 values a row; four lanes share
 // a block. A workgroup's four waves are stacked along the rows, so that 16 rows'
-// scale dwords of a plane are written side by side; it walks PL planes.
+// scale dwords of a plane are written side by side; it takes kQuantPlanes planes,
+// whose loads all go out before the first is used (a wave has 4 KiB in flight).
 constexpr int kQuantRows = 16, kQuantPlanes = 4;
 
 template <int DT>
@@ -56,19 +57,22 @@ mx4_quantize_kernel(const uint16_t *__restrict__ X, uint32_t *__restrict__ codes
                     uint32_t *__restrict__ scales, int M, int K) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     const long long row = (long long)blockIdx.x * kQuantRows + wid * 4 + (lane >> 4);
-    const int planes = ceil_div(K, 128);
     if (row >= M) return;   // whole 16-lane groups, so no block loses a lane
+    const int plane0 = blockIdx.y * kQuantPlanes, k0 = plane0 * 128 + (lane & 15) * 8;
+    const uint16_t *const x = X + (size_t)row * K;
+    u32x4 v[kQuantPlanes];
 #pragma unroll
     for (int p = 0; p < kQuantPlanes; ++p) {
-        const int plane = blockIdx.y * kQuantPlanes + p;
-        if (plane >= planes) break;
-        const int k = plane * 128 + (lane & 15) * 8;
-        u32x4 x = {0u, 0u, 0u, 0u};
-        if (k < K) x = *reinterpret_cast<const u32x4 *>(X + (size_t)row * K + k);
+        const int k = k0 + p * 128;
+        v[p] = k < K ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + k)) : u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int p = 0; p < kQuantPlanes; ++p) {
+        const int k = k0 + p * 128;
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t m = x[i] & 0x7fff7fffu;
+            const uint32_t m = v[p][i] & 0x7fff7fffu;
             top = max(top, max(m & 0xffffu, m >> 16));
         }
         top = max(top, (uint32_t)__shfl_xor((int)top, 1));
@@ -77,17 +81,17 @@ mx4_quantize_kernel(const uint16_t *__restrict__ X, uint32_t *__restrict__ codes
         const float sc = scale_value(s == 255u ? 127u : s);
         const bool tiny = s == 0u;
         uint32_t c = 0;
-        c = to_codes<DT, 0>(c, x[0], sc, tiny);
-        c = to_codes<DT, 1>(c, x[1], sc, tiny);
-        c = to_codes<DT, 2>(c, x[2], sc, tiny);
-        c = to_codes<DT, 3>(c, x[3], sc, tiny);
+        c = to_codes<DT, 0>(c, v[p][0], sc, tiny);
+        c = to_codes<DT, 1>(c, v[p][1], sc, tiny);
+        c = to_codes<DT, 2>(c, v[p][2], sc, tiny);
+        c = to_codes<DT, 3>(c, v[p][3], sc, tiny);
         if (s == 255u) c = 0;
         if (k < K) codes[((size_t)row * K + k) >> 3] = c;
         // The four blocks' bytes, into the first lane of the row.
         uint32_t w = k < K ? s << (8 * ((lane >> 2) & 3)) : 0u;
         w |= (uint32_t)__shfl_xor((int)w, 4);
         w |= (uint32_t)__shfl_xor((int)w, 8);
-        if ((lane & 15) == 0) scales[(size_t)plane * M + row] = w;
+        if ((lane & 15) == 0 && (plane0 + p) * 128 < K) scales[(size_t)(plane0 + p) * M + row] = w;
     }
 }
 
@@ -97,25 +101,27 @@ mx4_dequantize_kernel(const uint32_t *__restrict__ codes, const uint32_t *__rest
                       uint16_t *__restrict__ X, int M, int K) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     const long long row = (long long)blockIdx.x * kQuantRows + wid * 4 + (lane >> 4);
-    const int planes = ceil_div(K, 128);
     if (row >= M) return;
+    const int plane0 = blockIdx.y * kQuantPlanes, k0 = plane0 * 128 + (lane & 15) * 8;
+    uint32_t c[kQuantPlanes], w[kQuantPlanes];
 #pragma unroll
     for (int p = 0; p < kQuantPlanes; ++p) {
-        const int plane = blockIdx.y * kQuantPlanes + p;
-        if (plane >= planes) break;
-        const int k = plane * 128 + (lane & 15) * 8;
-        if (k >= K) break;
-        const uint32_t c = codes[((size_t)row * K + k) >> 3];
-        const uint32_t w = scales[(size_t)plane * M + row];
-        const float sc = scale_value((w >> (8 * ((lane >> 2) & 3))) & 255u);
+        const int k = k0 + p * 128;
+        c[p] = k < K ? codes[((size_t)row * K + k) >> 3] : 0u;
+        w[p] = k < K ? scales[(size_t)(plane0 + p) * M + row] : 0u;
+    }
+#pragma unroll
+    for (int p = 0; p < kQuantPlanes; ++p) {
+        const int k = k0 + p * 128;
+        const float sc = scale_value((w[p] >> (8 * ((lane >> 2) & 3))) & 255u);
         // The codes' values exactly, then one product (exact but for the ends of fp32's range).
-        const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
-        const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
-        const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
-        const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+        const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[p], 1.0f, 0);
+        const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[p], 1.0f, 1);
+        const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[p], 1.0f, 2);
+        const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[p], 1.0f, 3);
         const u32x4 y = {pack2<DT>(v0[0] * sc, v0[1] * sc), pack2<DT>(v1[0] * sc, v1[1] * sc),
                          pack2<DT>(v2[0] * sc, v2[1] * sc), pack2<DT>(v3[0] * sc, v3[1] * sc)};
-        *reinterpret_cast<u32x4 *>(X + (size_t)row * K + k) = y;
+        if (k < K) __builtin_nontemporal_store(y, reinterpret_cast<u32x4 *>(X + (size_t)row * K + k));
     }
 }
 

@@ -18,7 +18,9 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import GbaError, TRANSPOSE_B, _act, _check_dev, _dtype_code, _torch, _ws_args
+import torch
+
+from . import GbaError, TRANSPOSE_B, _act, _check_dev, _dtype_code
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 EXPERTS_LIB_PATH = os.path.join(_HERE, "libgba_experts.so")
@@ -67,17 +69,33 @@ def experts_version() -> str:
     return _lib().gbx_version().decode()
 
 
-def _call(fn_name, dev, *args):
-    """Run entry point fn_name on dev's current stream (see the package's _call)."""
-    torch = _torch()
+# The calls below run in a few microseconds of host time, as long as the smallest
+# kernels: the checks are written for that (attributes once, torch.Size compared as
+# the tuple it is, no copies of shapes).
+
+def _device(*ts):
+    """The index of the tensors' one device; _check_dev's refusals otherwise."""
+    d = ts[0].get_device()
+    if d >= 0:
+        for t in ts:
+            if t is not None and (t.get_device() != d or not t.is_contiguous()):
+                break
+        else:
+            return d
+    _check_dev(*ts)
+    raise ValueError("gba works on device tensors")
+
+
+def _call(fn_name, d, *args):
+    """Run entry point fn_name on device d's current stream (see the package's _call)."""
     lib = _LIB or _lib()
     C = torch._C
-    if dev.index == C._cuda_getDevice():
-        lib.gbx_set_stream(C._cuda_getCurrentRawStream(dev.index))
+    if d == C._cuda_getDevice():
+        lib.gbx_set_stream(C._cuda_getCurrentRawStream(d))
         st = getattr(lib, fn_name)(*args)
     else:
-        with torch.cuda.device(dev):
-            lib.gbx_set_stream(C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(d):
+            lib.gbx_set_stream(C._cuda_getCurrentRawStream(d))
             st = getattr(lib, fn_name)(*args)
     if st != 0:
         raise GbaError(st, fn_name)
@@ -87,30 +105,35 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(workspace):
+def _workspace(workspace, d):
     if workspace is None:
         return None, 0
-    _check_dev(workspace)
-    return _ws_args(workspace)
+    if workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError("the workspace is a contiguous tensor on the operands' device")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _offsets(offsets, E):
-    if offsets.dtype != _torch().int32:
+    if offsets.dtype is not torch.int32:
         raise TypeError("offsets are int32, got %s" % offsets.dtype)
-    if tuple(offsets.shape) != (E + 1,):
+    if offsets.shape != (E + 1,):
         raise ValueError("offsets has E + 1 = %d entries, got shape %s" % (E + 1, tuple(offsets.shape)))
 
 
+_CODES = {torch.float16: 0, torch.bfloat16: 1}
+
+
 def _same_dtype(first, *rest):
-    dt = _dtype_code(first)
+    dtype = first.dtype
     for t in rest:
-        if t is not None and t.dtype != first.dtype:
+        if t is not None and t.dtype is not dtype:
             raise TypeError("all operands must share one dtype")
-    return dt
+    dt = _CODES.get(dtype)
+    return _dtype_code(first) if dt is None else dt
 
 
 def _expect(what, t, shape):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError("shape mismatch: %s is %s, expected %s" % (what, tuple(t.shape), shape))
 
 
@@ -123,18 +146,22 @@ def grouped_gemm_bias_act(a, offsets, w, bias, c, act="gelu", transpose_b=False,
     rounded (grouped_gemm_act_grad's z). Rows of no expert are not written.
     workspace: optional device tensor (a few MiB) that lets calls with few output
     tiles split K."""
-    dev = _check_dev(a, offsets, w, bias, c, preact)
+    d = _device(a, offsets, w, bias, c, preact)
     dt = _same_dtype(a, w, bias, c, preact)
     T, K = a.shape
-    E, N = w.shape[0], w.shape[1 if transpose_b else 2]
-    _expect("w", w, (E, N, K) if transpose_b else (E, K, N))
+    if transpose_b:
+        E, N, k = w.shape
+    else:
+        E, k, N = w.shape
+    if k != K:
+        raise ValueError("shape mismatch: a is %s, w %s" % (tuple(a.shape), tuple(w.shape)))
     _expect("c", c, (T, N))
     _expect("bias", bias, (E, N))
     _expect("preact", preact, (T, N))
     _offsets(offsets, E)
-    ws, nb = _workspace(workspace)
-    _call("grouped_gemm_bias_act", dev, _addr(a), _addr(offsets), _addr(w), _addr(bias), _addr(c),
-          _addr(preact), T, E, N, K, _act(act), dt, TRANSPOSE_B if transpose_b else 0, ws, nb)
+    ws, nb = _workspace(workspace, d)
+    _call("grouped_gemm_bias_act", d, a.data_ptr(), offsets.data_ptr(), w.data_ptr(), _addr(bias),
+          c.data_ptr(), _addr(preact), T, E, N, K, _act(act), dt, TRANSPOSE_B if transpose_b else 0, ws, nb)
     return c
 
 
@@ -145,17 +172,21 @@ def grouped_gemm_act_grad(dc, offsets, w, z, da, act="gelu", transpose_b=False, 
 
     w and transpose_b as in the forward call; dc [T,N]; z, da [T,K]. act "none":
     da = dc @ w[e].T, and z may be None."""
-    dev = _check_dev(dc, offsets, w, z, da)
+    d = _device(dc, offsets, w, z, da)
     dt = _same_dtype(dc, w, z, da)
     T, N = dc.shape
-    E, K = w.shape[0], w.shape[2 if transpose_b else 1]
-    _expect("w", w, (E, N, K) if transpose_b else (E, K, N))
+    if transpose_b:
+        E, n, K = w.shape
+    else:
+        E, K, n = w.shape
+    if n != N:
+        raise ValueError("shape mismatch: dc is %s, w %s" % (tuple(dc.shape), tuple(w.shape)))
     _expect("da", da, (T, K))
     _expect("z", z, (T, K))
     _offsets(offsets, E)
-    ws, nb = _workspace(workspace)
-    _call("grouped_gemm_act_grad", dev, _addr(dc), _addr(offsets), _addr(w), _addr(z), _addr(da),
-          T, E, N, K, _act(act), dt, TRANSPOSE_B if transpose_b else 0, ws, nb)
+    ws, nb = _workspace(workspace, d)
+    _call("grouped_gemm_act_grad", d, dc.data_ptr(), offsets.data_ptr(), w.data_ptr(), _addr(z),
+          da.data_ptr(), T, E, N, K, _act(act), dt, TRANSPOSE_B if transpose_b else 0, ws, nb)
     return da
 
 
@@ -167,8 +198,7 @@ def grouped_gemm_wgrad(a, dc, offsets, dw, dbias=None, accumulate=False, transpo
     a [T,K], dc [T,N], of one 16-bit dtype; dw and dbias of that dtype or both
     float32. accumulate (float32 only): added to what they hold. An empty expert's
     gradients are zero."""
-    torch = _torch()
-    dev = _check_dev(a, dc, offsets, dw, dbias)
+    d = _device(a, dc, offsets, dw, dbias)
     dt = _same_dtype(a, dc)
     T, K = a.shape
     N, E = dc.shape[1], dw.shape[0]
@@ -177,19 +207,19 @@ def grouped_gemm_wgrad(a, dc, offsets, dw, dbias=None, accumulate=False, transpo
     _expect("dbias", dbias, (E, N))
     _offsets(offsets, E)
     flags = TRANSPOSE_B if transpose_b else 0
-    if dw.dtype == torch.float32:
+    if dw.dtype is torch.float32:
         flags |= OUT_F32
-    elif dw.dtype != a.dtype:
+    elif dw.dtype is not a.dtype:
         raise TypeError("dw has the operands' dtype or float32")
-    if dbias is not None and dbias.dtype != dw.dtype:
+    if dbias is not None and dbias.dtype is not dw.dtype:
         raise TypeError("dbias has dw's dtype")
     if accumulate:
-        if dw.dtype != torch.float32:
+        if dw.dtype is not torch.float32:
             raise TypeError("accumulate needs float32 gradients")
         flags |= ACCUMULATE
-    ws, nb = _workspace(workspace)
-    _call("grouped_gemm_wgrad", dev, _addr(a), _addr(dc), _addr(offsets), _addr(dw), _addr(dbias),
-          T, E, N, K, dt, flags, ws, nb)
+    ws, nb = _workspace(workspace, d)
+    _call("grouped_gemm_wgrad", d, a.data_ptr(), dc.data_ptr(), offsets.data_ptr(), dw.data_ptr(),
+          _addr(dbias), T, E, N, K, dt, flags, ws, nb)
     return dw
 
 
@@ -201,7 +231,6 @@ def mx4_scales_shape(M: int, K: int) -> tuple:
 def mx4_pack_scales(rows):
     """Scale planes of scale bytes given by rows ([M, K/32] uint8, the layout of the
     OCP MX specification's blocks in row order)."""
-    torch = _torch()
     M, blocks = rows.shape
     planes = -(-blocks // 4)
     full = torch.zeros(M, planes * 4, dtype=torch.uint8, device=rows.device)
@@ -215,40 +244,41 @@ def mx4_unpack_scales(scales, K: int):
 
 
 def _mx4(what, codes, scales, M, K):
-    torch = _torch()
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise TypeError("4-bit codes and scales are uint8 tensors")
     if K % 32:
         raise ValueError("%s: K must be a multiple of 32, got %d" % (what, K))
     if codes.numel() != M * K // 2:
         raise ValueError("%s: %d rows of %d codes are %d bytes, got shape %s" % (what, M, K, M * K // 2,
                                                                                  tuple(codes.shape)))
-    _expect(what + " scales", scales, (-(-K // 128), M, 4))
+    if scales.shape != (-(-K // 128), M, 4):
+        raise ValueError("shape mismatch: %s scales are %s, expected %s" % (what, tuple(scales.shape),
+                                                                          mx4_scales_shape(M, K)))
 
 
 def mx4_quantize(x, codes, scales):
     """Quantise x [M,K] (float16 or bfloat16, K a multiple of 32) to microscaled 4-bit
     floats: codes uint8 [M,K/2], scales uint8 [ceil(K/128),M,4]. Returns (codes, scales)."""
-    dev = _check_dev(x, codes, scales)
+    d = _device(x, codes, scales)
     M, K = x.shape
     _mx4("codes", codes, scales, M, K)
-    _call("mx4_quantize", dev, _addr(x), _addr(codes), _addr(scales), M, K, _dtype_code(x))
+    _call("mx4_quantize", d, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K, _same_dtype(x))
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, x):
     """x [M,K] (float16 or bfloat16) = the values of codes and scales. Returns x."""
-    dev = _check_dev(codes, scales, x)
+    d = _device(codes, scales, x)
     M, K = x.shape
     _mx4("codes", codes, scales, M, K)
-    _call("mx4_dequantize", dev, _addr(codes), _addr(scales), _addr(x), M, K, _dtype_code(x))
+    _call("mx4_dequantize", d, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), M, K, _same_dtype(x))
     return x
 
 
 def gemm_bias_act_mx4(a_codes, a_scales, w_codes, w_scales, bias, c, act="gelu", workspace=None):
     """c[M,N] = act(a @ w.T + bias) with a [M,K] and w [N,K] as mx4_quantize leaves
     them; bias [N] or None and c float16 or bfloat16. Returns c."""
-    dev = _check_dev(a_codes, a_scales, w_codes, w_scales, bias, c)
+    d = _device(a_codes, a_scales, w_codes, w_scales, bias, c)
     dt = _same_dtype(c, bias)
     (M, half), N = a_codes.shape, c.shape[1]
     K = 2 * half
@@ -257,9 +287,9 @@ def gemm_bias_act_mx4(a_codes, a_scales, w_codes, w_scales, bias, c, act="gelu",
     _expect("bias", bias, (N,))
     _mx4("a", a_codes, a_scales, M, K)
     _mx4("w", w_codes, w_scales, N, K)
-    ws, nb = _workspace(workspace)
-    _call("gemm_bias_act_mx4", dev, _addr(a_codes), _addr(a_scales), _addr(w_codes), _addr(w_scales),
-          _addr(bias), _addr(c), M, N, K, _act(act), dt, ws, nb)
+    ws, nb = _workspace(workspace, d)
+    _call("gemm_bias_act_mx4", d, a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
+          w_scales.data_ptr(), _addr(bias), c.data_ptr(), M, N, K, _act(act), dt, ws, nb)
     return c
 
 
@@ -267,17 +297,18 @@ def grouped_gemm_bias_act_mx4(a_codes, a_scales, offsets, w_codes, w_scales, bia
                               workspace=None):
     """gemm_bias_act_mx4 by expert: a [T,K] sorted by expert, w_codes [E,N,K/2] with the
     scale planes of the [E*N,K] matrix, bias [E,N] or None. Returns c."""
-    dev = _check_dev(a_codes, a_scales, offsets, w_codes, w_scales, bias, c)
+    d = _device(a_codes, a_scales, offsets, w_codes, w_scales, bias, c)
     dt = _same_dtype(c, bias)
-    (T, half), (E, N, _) = a_codes.shape, w_codes.shape
+    (T, half), (E, N, wide) = a_codes.shape, w_codes.shape
+    if wide != half:
+        raise ValueError("shape mismatch: a is %s, w %s" % (tuple(a_codes.shape), tuple(w_codes.shape)))
     K = 2 * half
     _expect("c", c, (T, N))
-    _expect("w_codes", w_codes, (E, N, half))
     _expect("bias", bias, (E, N))
     _mx4("a", a_codes, a_scales, T, K)
     _mx4("w", w_codes, w_scales, E * N, K)
     _offsets(offsets, E)
-    ws, nb = _workspace(workspace)
-    _call("grouped_gemm_bias_act_mx4", dev, _addr(a_codes), _addr(a_scales), _addr(offsets),
-          _addr(w_codes), _addr(w_scales), _addr(bias), _addr(c), T, E, N, K, _act(act), dt, ws, nb)
+    ws, nb = _workspace(workspace, d)
+    _call("grouped_gemm_bias_act_mx4", d, a_codes.data_ptr(), a_scales.data_ptr(), offsets.data_ptr(),
+          w_codes.data_ptr(), w_scales.data_ptr(), _addr(bias), c.data_ptr(), T, E, N, K, _act(act), dt, ws, nb)
     return c
