@@ -232,62 +232,96 @@ grouped_ring_kernel(Group g) {
         compute(stage);
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    wait_vmcnt<0>();   // no direct-to-LDS write may outlive the workgroup's LDS
-
-    // ---- epilogue: lane l holds row l % 16, columns 4 (l / 16) .. +3 of each block ----
+    // ---- epilogue ----
+    // The tile's fp32 sums go through the ring's LDS (a lane: one row, four adjacent
+    // columns) to threads of eight adjacent columns, so that every global access of the
+    // epilogue is 16 bytes a lane and whole 128-byte lines: writing a weight
+    // gradient's tile from the matrix layout (32 bytes a row) took 1.6 times as long.
+    // Chunk q (16 bytes) of row r lies at q ^ (r % 8).
+    wait_vmcnt_lgkm0<0>();
+    block_barrier();   // every wave's loads have landed and its reads are done
+    constexpr int QN = BN / 4, TC = BN / 8, UNITS = BM * TC / NT > 0 ? BM * TC / NT : 1;
+    static_assert(BM * BN * 4 <= STAGES * STAGE, "the sums fit the ring");
+    static_assert(NT % TC == 0, "a thread keeps its columns");
+#pragma unroll
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+        for (int b = 0; b < FM; ++b) {
+            const int r = wm * WTM + b * 16 + tj, q = (wn * WTN + a * 16) / 4 + tg;
+            *reinterpret_cast<f32x4 *>(smem + (r * QN + (q ^ (r & 7))) * 16) = acc[a][b];
+        }
+    wait_vmcnt_lgkm0<0>();
+    block_barrier();
+    const int col = tid % TC, n = n0 + col * 8;
     const size_t crow = TA ? (size_t)e * M : (size_t)start;
-    auto each_block = [&](auto &&f) __attribute__((always_inline)) {
+    // f(the eight sums of row m0 + r from column n on, their place in the output)
+    auto each = [&](auto &&f) __attribute__((always_inline)) {
 #pragma unroll
-        for (int a = 0; a < FN; ++a) {
-            const int n = n0 + wn * WTN + a * 16 + 4 * tg;
-            if (n >= N) continue;
-#pragma unroll
-            for (int b = 0; b < FM; ++b) {
-                const int m = m0 + wm * WTM + b * 16 + tj;
-                if (m >= M) continue;
-                f(acc[a][b], n, (crow + m) * (size_t)N + n);
-            }
+        for (int u = 0; u < UNITS; ++u) {
+            const int r = u * (NT / TC) + tid / TC;
+            if (r >= rows_a || n >= N) continue;   // N is a multiple of 8
+            const int q = 2 * col;
+            f32x4 v[2] = {*reinterpret_cast<const f32x4 *>(smem + (r * QN + (q ^ (r & 7))) * 16),
+                          *reinterpret_cast<const f32x4 *>(smem + (r * QN + ((q + 1) ^ (r & 7))) * 16)};
+            f(v, (crow + m0 + r) * (size_t)N + n);
         }
     };
-    auto four = [](const uint16_t *p) __attribute__((always_inline)) {
-        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-        return f32x4{to_f32<ODT>(v.x & 0xffffu), to_f32<ODT>(v.x >> 16), to_f32<ODT>(v.y & 0xffffu), to_f32<ODT>(v.y >> 16)};
+    auto eight = [](const uint16_t *p, f32x4 (&v)[2]) __attribute__((always_inline)) {
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i / 2][2 * (i % 2)] = to_f32<ODT>(x[i] & 0xffffu);
+            v[i / 2][2 * (i % 2) + 1] = to_f32<ODT>(x[i] >> 16);
+        }
     };
-    auto store4 = [](uint16_t *p, const f32x4 &v) __attribute__((always_inline)) {
-        *reinterpret_cast<u32x2 *>(p) = u32x2{pack2<ODT>(v[0], v[1]), pack2<ODT>(v[2], v[3])};
+    auto store8 = [](uint16_t *p, const f32x4 (&v)[2]) __attribute__((always_inline)) {
+        const u32x4 x = {pack2<ODT>(v[0][0], v[0][1]), pack2<ODT>(v[0][2], v[0][3]),
+                         pack2<ODT>(v[1][0], v[1][1]), pack2<ODT>(v[1][2], v[1][3])};
+        __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(p));
     };
     if constexpr (EPI == EPI_PART) {
         float *const P = g.part + (size_t)split * (TA ? (size_t)g.E * M : (size_t)g.T) * N;
-        each_block([&](const f32x4 &a, int, size_t at) { *reinterpret_cast<f32x4 *>(P + at) = a; });
+        each([&](f32x4 (&v)[2], size_t at) {
+            *reinterpret_cast<f32x4 *>(P + at) = v[0];
+            *reinterpret_cast<f32x4 *>(P + at + 4) = v[1];
+        });
     } else if constexpr (EPI == EPI_ACT) {
-        const uint16_t *const bias = g.bias ? g.bias + (size_t)e * N : nullptr;
+        f32x4 bias[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+        if (g.bias && n < N) eight(g.bias + (size_t)e * N + n, bias);
         with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act_c)::value;
-            each_block([&](f32x4 a, int n, size_t at) {
-                if (bias) a += four(bias + n);
-                if (g.zout) store4(g.zout + at, a);
-                store4((uint16_t *)g.C + at, f32x4{act_fn<ACT>(a[0]), act_fn<ACT>(a[1]), act_fn<ACT>(a[2]), act_fn<ACT>(a[3])});
+            each([&](f32x4 (&v)[2], size_t at) {
+                v[0] += bias[0];
+                v[1] += bias[1];
+                if (g.zout) store8(g.zout + at, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = act_fn<ACT>(v[i / 4][i % 4]);
+                store8((uint16_t *)g.C + at, v);
             });
         });
     } else if constexpr (EPI == EPI_SLOPE) {
         with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act_c)::value;
-            each_block([&](f32x4 a, int, size_t at) {
+            each([&](f32x4 (&v)[2], size_t at) {
                 if constexpr (ACT != ACT_NONE) {
-                    const f32x4 z = four(g.z + at);
-                    a *= f32x4{act_slope<ACT>(z[0]), act_slope<ACT>(z[1]), act_slope<ACT>(z[2]), act_slope<ACT>(z[3])};
+                    f32x4 z[2];
+                    eight(g.z + at, z);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i / 4][i % 4] *= act_slope<ACT>(z[i / 4][i % 4]);
                 }
-                store4((uint16_t *)g.C + at, a);
+                store8((uint16_t *)g.C + at, v);
             });
         });
     } else {
         if (g.flags & GF_F32) {
-            each_block([&](f32x4 a, int, size_t at) {
+            each([&](f32x4 (&v)[2], size_t at) {
                 f32x4 *const p = reinterpret_cast<f32x4 *>((float *)g.C + at);
-                *p = (g.flags & GF_ADD) ? a + *p : a;
+                const bool add = (g.flags & GF_ADD) != 0;
+                p[0] = add ? p[0] + v[0] : v[0];
+                p[1] = add ? p[1] + v[1] : v[1];
             });
         } else {
-            each_block([&](const f32x4 &a, int, size_t at) { store4((uint16_t *)g.C + at, a); });
+            each([&](f32x4 (&v)[2], size_t at) { store8((uint16_t *)g.C + at, v); });
         }
     }
 }
