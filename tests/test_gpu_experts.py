@@ -37,6 +37,16 @@ def guarded(shape, dtype, fill=float("nan")):
     return whole[2048:2048 + n].view(shape), intact
 
 
+def workspace(size=8 << 20):
+    """A workspace of NaN, and a check that nothing past it was written."""
+    whole = torch.full((size // 4 + 1024,), float("nan"), device="cuda")
+    whole[size // 4:] = 7.0
+
+    def intact():
+        assert (whole[size // 4:] == 7).all(), "written outside the workspace"
+    return whole[:size // 4], intact
+
+
 def make_offsets(sizes, lead=0):
     o = [lead]
     for n in sizes:
@@ -71,6 +81,18 @@ BIG = [
     ([4096], 1, 0, 3080, 264),
     ([300, 2000, 1, 0, 1000, 640], 0, 2, 4104, 1000),
 ]
+# Few output tiles and a long sum: split over K where a workspace is given.
+DEEP = [
+    ([3, 0, 20], 1, 2, 264, 4096),
+    ([100], 0, 0, 256, 4104),
+    ([1], 0, 0, 72, 3080),
+    ([0, 70, 0, 1], 0, 3, 520, 2056),
+]
+DEEP_GRAD = [
+    ([5000], 0, 0, 136, 200),
+    ([1500, 0, 3], 1, 1, 72, 264),
+    ([3000, 700], 0, 2, 512, 320),
+]
 BIG_GRAD = [
     ([257, 0, 511, 1, 64], 0, 0, 2056, 1544),
     ([65, 1000, 63, 300], 2, 5, 1800, 2048),
@@ -85,9 +107,9 @@ def build(seed, sizes, lead, tail, dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("tb", [True, False])
-@pytest.mark.parametrize("i", range(len(SHAPES + BIG)))
+@pytest.mark.parametrize("i", range(len(SHAPES + BIG + DEEP)))
 def test_forward(i, tb, dtype):
-    sizes, lead, tail, N, K = (SHAPES + BIG)[i]
+    sizes, lead, tail, N, K = (SHAPES + BIG + DEEP)[i]
     dt, act = DT[dtype], orc.ACTS[(i + tb) % 6]
     say("forward", i, sizes[:8], N, K, tb, dtype, act)
     g, off, T, E = build(100 + i, sizes, lead, tail, dt)
@@ -111,13 +133,21 @@ def test_forward(i, tb, dtype):
     c2, _ = guarded((T, N), dt)
     gba.grouped_gemm_bias_act(a, off, w, bias, c2, act, transpose_b=tb)
     assert torch.equal(c2[owned], c[owned])
+    c3, intact = guarded((T, N), dt)
+    z3, z3_intact = guarded((T, N), dt)
+    ws, ws_intact = workspace()
+    gba.grouped_gemm_bias_act(a, off, w, bias, c3, act, transpose_b=tb, preact=z3, workspace=ws)
+    torch.cuda.synchronize()
+    intact(), z3_intact(), ws_intact()
+    orc.check("preact, workspace", z3, want_z, orc.with_rounding(want_z, err, dt), owned)
+    orc.check("c, workspace", c3, want, orc.with_rounding(want, orc.LIPSCHITZ[act] * err + orc.ACT_TOL, dt), owned)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("tb", [True, False])
-@pytest.mark.parametrize("i", range(len(SHAPES + BIG)))
+@pytest.mark.parametrize("i", range(len(SHAPES + BIG + DEEP)))
 def test_act_grad(i, tb, dtype):
-    sizes, lead, tail, K, N = (SHAPES + BIG)[i]
+    sizes, lead, tail, K, N = (SHAPES + BIG + DEEP)[i]
     dt, act = DT[dtype], orc.ACTS[(i + 2 * tb) % 6]
     say("act_grad", i, sizes[:8], N, K, tb, dtype, act)
     g, off, T, E = build(200 + i, sizes, lead, tail, dt)
@@ -134,14 +164,20 @@ def test_act_grad(i, tb, dtype):
     tol = 0.0 if z is None else orc.SLOPE_TOL
     bound = orc.with_rounding(d * s, s.abs() * err + tol * (d.abs() + err), dt)
     orc.check("da", da, d * s, bound, owned)
+    da2, intact = guarded((T, K), dt)
+    ws, ws_intact = workspace()
+    gba.grouped_gemm_act_grad(dc, off, w, z, da2, act, transpose_b=tb, workspace=ws)
+    torch.cuda.synchronize()
+    intact(), ws_intact()
+    orc.check("da, workspace", da2, d * s, bound, owned)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("tb", [True, False])
 @pytest.mark.parametrize("out", ["own", "f32", "add"])
-@pytest.mark.parametrize("i", range(len(SHAPES + BIG_GRAD)))
+@pytest.mark.parametrize("i", range(len(SHAPES + BIG_GRAD + DEEP_GRAD)))
 def test_wgrad(i, out, tb, dtype):
-    sizes, lead, tail, N, K = (SHAPES + BIG_GRAD)[i]
+    sizes, lead, tail, N, K = (SHAPES + BIG_GRAD + DEEP_GRAD)[i]
     dt = DT[dtype]
     say("wgrad", i, sizes[:8], N, K, out, tb, dtype)
     g, off, T, E = build(300 + i, sizes, lead, tail, dt)
@@ -167,6 +203,12 @@ def test_wgrad(i, out, tb, dtype):
     w_intact(), b_intact()
     orc.check("dw", dw if tb else dw.transpose(1, 2), want, bound)
     orc.check("dbias", db, want_b, bound_b)
+    dw2, intact = guarded(dw.shape, odt, fill)
+    ws, ws_intact = workspace()
+    gba.grouped_gemm_wgrad(a, dc, off, dw2, None, accumulate=out == "add", transpose_b=tb, workspace=ws)
+    torch.cuda.synchronize()
+    intact(), ws_intact()
+    orc.check("dw, workspace", dw2 if tb else dw2.transpose(1, 2), want, bound)
     again = torch.full_like(dw, fill)
     gba.grouped_gemm_wgrad(a, dc, off, again, None, accumulate=out == "add", transpose_b=tb)
     assert torch.equal(again, dw)

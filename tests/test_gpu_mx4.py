@@ -4,7 +4,7 @@ import pytest
 import tiled_dense_gemm_bias_amd as gba
 from tests import experts_oracle as orc
 from tests.gpu_util import say
-from tests.test_gpu_experts import DT, draw, guarded, make_offsets
+from tests.test_gpu_experts import DT, draw, guarded, make_offsets, workspace
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -88,7 +88,8 @@ def test_quantise_every_value(dtype):
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 8, 32), (1, 1000, 4096), (5, 264, 96), (16, 64, 256), (17, 72, 288), (63, 136, 544),
                                    (65, 200, 1024), (129, 264, 160), (300, 520, 2080), (513, 1032, 128),
-                                   (1025, 10248, 288), (3000, 5128, 544), (4096, 4096, 512), (8200, 2056, 1312)])
+                                   (1025, 10248, 288), (3000, 5128, 544), (4096, 4096, 512), (8200, 2056, 1312),
+                                   (3, 264, 8192), (40, 136, 4128), (150, 72, 10240)])
 def test_product(M, N, K, dtype):
     dt, act = DT[dtype], orc.ACTS[(M + N) % 6]
     say("mx4 product", M, N, K, dtype, act)
@@ -105,13 +106,20 @@ def test_product(M, N, K, dtype):
     intact()
     want = orc.act(act, want_z)
     orc.check("c", c, want, orc.with_rounding(want, orc.LIPSCHITZ[act] * err + orc.ACT_TOL, dt))
+    c2, intact = guarded((M, N), dt)
+    ws, ws_intact = workspace()
+    gba.gemm_bias_act_mx4(ac, asc, wc, wsc, bias, c2, act, workspace=ws)
+    torch.cuda.synchronize()
+    intact(), ws_intact()
+    orc.check("c, workspace", c2, want, orc.with_rounding(want, orc.LIPSCHITZ[act] * err + orc.ACT_TOL, dt))
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("sizes,lead,tail,N,K", [
     ([1], 0, 0, 8, 32), ([0, 3, 0, 1], 1, 0, 72, 160), ([5, 0, 16, 17], 0, 3, 136, 96), ([63, 0, 65, 2], 2, 1, 200, 544),
     ([129, 255, 0, 130], 0, 5, 264, 288), ([1] * 70 + [0] * 20 + [3] * 20, 0, 0, 40, 128),
-    ([257, 0, 511, 300, 1000], 0, 0, 8200, 288), ([200] * 70, 0, 3, 1032, 544), ([300, 2000, 1, 0, 1000, 640], 5, 0, 4104, 1056)])
+    ([257, 0, 511, 300, 1000], 0, 0, 8200, 288), ([200] * 70, 0, 3, 1032, 544), ([300, 2000, 1, 0, 1000, 640], 5, 0, 4104, 1056),
+    ([3, 0, 20], 1, 2, 264, 8224)])
 def test_grouped_product(sizes, lead, tail, N, K, dtype):
     dt, act = DT[dtype], orc.ACTS[len(sizes) % 6]
     say("mx4 grouped", sizes[:8], lead, tail, N, K, dtype, act)
@@ -132,6 +140,12 @@ def test_grouped_product(sizes, lead, tail, N, K, dtype):
     intact()
     want = orc.act(act, want_z)
     orc.check("c", c, want, orc.with_rounding(want, orc.LIPSCHITZ[act] * err + orc.ACT_TOL, dt), owned)
+    c2, intact = guarded((T, N), dt)
+    ws, ws_intact = workspace()
+    gba.grouped_gemm_bias_act_mx4(ac, asc, off, wc.view(E, N, K // 2), wsc, bias, c2, act, workspace=ws)
+    torch.cuda.synchronize()
+    intact(), ws_intact()
+    orc.check("c, workspace", c2, want, orc.with_rounding(want, orc.LIPSCHITZ[act] * err + orc.ACT_TOL, dt), owned)
 
 
 def test_product_of_scales_over_the_whole_range():

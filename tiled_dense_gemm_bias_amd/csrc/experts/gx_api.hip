@@ -5,9 +5,11 @@
 #include <mutex>
 
 #include "gba_experts.h"
+#include "gx_colsum.hpp"
 #include "gx_launch.hpp"
 #include "gx_mx4.hpp"
-#include "gx_colsum.hpp"
+#include "gx_plan.hpp"
+#include "gx_reduce.hpp"
 
 #define GBX_VERSION_STRING "0.1.0"
 
@@ -93,18 +95,17 @@ int check_sizes(int64_t T, int64_t E, int64_t depth, int64_t width) {
 
 size_t size3(int64_t a, int64_t b, int64_t c) { return (size_t)a * (size_t)b * (size_t)c; }
 
-// Whether 256 x 256 tiles (persistent kernel) fill the chip: rows of about
-// T / E an expert, `cols` columns, `slices` K slices.
-bool big_rows(int64_t T, int64_t E, int64_t cols, int64_t words) {
-    const int64_t some = E < T ? E : T, mean = T / some;
-    return words > 64 && mean >= 160 && (T / 256 + some / 2) * ((cols + 255) / 256) >= 192;
+// The ring kernel of a plan, then (a split) the second pass.
+int launch_split(gbx::Group &g, const gbx::Plan &p, const gbx::LaunchFn &whole, const gbx::LaunchFn &part,
+                 const gbx::LaunchFn &reduce, void *workspace) {
+    if (p.splits == 1) return hip_result(whole(g, t_stream));
+    g.splits = p.splits;
+    g.part = (float *)workspace;
+    const int s = hip_result(part(g, t_stream));
+    return s ? s : hip_result(reduce(g, t_stream));
 }
 
-// Tile for rows of about T / E an expert.
-int row_tile(int64_t T, int64_t E) {
-    const int64_t mean = T / (E < T ? E : T);
-    return mean <= 16 ? gbx::TILE_16x64 : mean <= 96 ? gbx::TILE_64x64 : gbx::TILE_128x128;
-}
+int current_cus(int *cus) { return hip_result(gba::current_cus(cus)); }
 
 }  // namespace
 
@@ -149,12 +150,17 @@ int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, 
     g.act = act;
     g.splits = 1;
     const bool nt = (flags & GBA_TRANSPOSE_B) != 0;
-    if (big_rows(T, E, N, K)) {
+    int cus;
+    if ((s = current_cus(&cus))) return s;
+    const gbx::Plan p = gbx::plan_rows(T, E, N, K, workspace ? workspace_bytes : 0, cus);
+    if (p.big) {
         const gbx::LaunchFn *const big[2][2] = {{gbx::big_fwd_nn_f16, gbx::big_fwd_nn_bf16},
                                                 {gbx::big_fwd_nt_f16, gbx::big_fwd_nt_bf16}};
         return hip_result(big[nt][dtype][act](g, t_stream));
     }
-    return hip_result((nt ? gbx::fwd_nt : gbx::fwd_nn)[dtype][row_tile(T, E)](g, t_stream));
+    const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_ACT, 0, false>, gbx::launch_reduce<gbx::EPI_ACT, 1, false>};
+    return launch_split(g, p, (nt ? gbx::fwd_nt : gbx::fwd_nn)[dtype][p.tile],
+                        (nt ? gbx::part_nt : gbx::part_nn)[dtype][p.tile], reduce[dtype], workspace);
 }
 
 int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W, const void *z,
@@ -188,12 +194,17 @@ int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W,
     g.splits = 1;
     // W [E,N,K] has its rows along the sum, W [E,K,N] its columns.
     const bool nt = !(flags & GBA_TRANSPOSE_B);
-    if (big_rows(T, E, K, N)) {
+    int cus;
+    if ((s = current_cus(&cus))) return s;
+    const gbx::Plan p = gbx::plan_rows(T, E, K, N, workspace ? workspace_bytes : 0, cus);
+    if (p.big) {
         const gbx::LaunchFn *const big[2][2] = {{gbx::big_slope_nn_f16, gbx::big_slope_nn_bf16},
                                                 {gbx::big_slope_nt_f16, gbx::big_slope_nt_bf16}};
         return hip_result(big[nt][dtype][act](g, t_stream));
     }
-    return hip_result((nt ? gbx::slope_nt : gbx::slope_nn)[dtype][row_tile(T, E)](g, t_stream));
+    const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_SLOPE, 0, false>, gbx::launch_reduce<gbx::EPI_SLOPE, 1, false>};
+    return launch_split(g, p, (nt ? gbx::slope_nt : gbx::slope_nn)[dtype][p.tile],
+                        (nt ? gbx::part_nt : gbx::part_nn)[dtype][p.tile], reduce[dtype], workspace);
 }
 
 int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, void *dW,
@@ -231,10 +242,12 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
         g.M = (int)(nk ? N : K);
         g.N = (int)(nk ? K : N);
         g.C = dW;
-        const int64_t tiles = E * ((g.M + 127) / 128) * ((g.N + 127) / 128);
-        const int tile = tiles >= 256 ? gbx::TILE_128x128 : gbx::TILE_64x64;
-        const bool big = E * ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 192 && T / E >= 128;
-        s = hip_result(big ? gbx::big_wgrad_tn[dtype][f32](g, t_stream) : gbx::wgrad_tn[dtype][tile](g, t_stream));
+        int cus;
+        if ((s = current_cus(&cus))) return s;
+        const gbx::Plan p = gbx::plan_grad(T, E, g.M, g.N, workspace ? workspace_bytes : 0, cus);
+        const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_GRAD, 0, true>, gbx::launch_reduce<gbx::EPI_GRAD, 1, true>};
+        s = p.big ? hip_result(gbx::big_wgrad_tn[dtype][f32](g, t_stream))
+                  : launch_split(g, p, gbx::wgrad_tn[dtype][p.tile], gbx::part_tn[dtype][p.tile], reduce[dtype], workspace);
         if (s) return s;
     }
     if (dbias) {
@@ -317,9 +330,13 @@ static int mx4_common(const void *a_codes, const void *a_scales, const int32_t *
     g.K = (int)(K / 4);   // 16-bit words of four codes
     g.act = act;
     g.splits = 1;
-    if (big_rows(T, E, N, K / 4))
+    int cus;
+    if ((s = current_cus(&cus))) return s;
+    const gbx::Plan p = gbx::plan_rows(T, E, N, K / 4, workspace ? workspace_bytes : 0, cus);
+    if (p.big)
         return hip_result((dtype == GBA_DTYPE_F16 ? gbx::big_mx4_f16 : gbx::big_mx4_bf16)[act](g, t_stream));
-    return hip_result(gbx::mx4_nt[dtype][row_tile(T, E)](g, t_stream));
+    const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_ACT, 0, false>, gbx::launch_reduce<gbx::EPI_ACT, 1, false>};
+    return launch_split(g, p, gbx::mx4_nt[dtype][p.tile], gbx::part_mx4[dtype][p.tile], reduce[dtype], workspace);
 }
 
 int gemm_bias_act_mx4(const void *a_codes, const void *a_scales, const void *w_codes,

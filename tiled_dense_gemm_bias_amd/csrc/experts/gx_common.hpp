@@ -203,6 +203,62 @@ __device__ __forceinline__ void with_act(int act, F &&f) {
     }
 }
 
+// ----------------------------------------------------- eight outputs at once --
+
+template <int DT>
+__device__ __forceinline__ void load8(const uint16_t *p, f32x4 (&v)[2]) {
+    const u32x4 x = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i / 2][2 * (i % 2)] = to_f32<DT>(x[i] & 0xffffu);
+        v[i / 2][2 * (i % 2) + 1] = to_f32<DT>(x[i] >> 16);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(uint16_t *p, const f32x4 (&v)[2]) {
+    const u32x4 x = {pack2<DT>(v[0][0], v[0][1]), pack2<DT>(v[0][2], v[0][3]),
+                     pack2<DT>(v[1][0], v[1][1]), pack2<DT>(v[1][2], v[1][3])};
+    __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(p));
+}
+
+// The epilogue of eight adjacent sums of one row of expert e, from column n on,
+// at place `at` of the output.
+template <int EPI, int ODT>
+__device__ __forceinline__ void finish(const Group &g, f32x4 (&v)[2], int e, int n, size_t at) {
+    if constexpr (EPI == EPI_ACT) {
+        if (g.bias) {
+            f32x4 bias[2];
+            load8<ODT>(g.bias + (size_t)e * g.N + n, bias);
+            v[0] += bias[0];
+            v[1] += bias[1];
+        }
+        if (g.zout) store8<ODT>(g.zout + at, v);
+        with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = act_fn<decltype(act_c)::value>(v[i / 4][i % 4]);
+        });
+        store8<ODT>((uint16_t *)g.C + at, v);
+    } else if constexpr (EPI == EPI_SLOPE) {
+        if (g.act != ACT_NONE) {
+            f32x4 z[2];
+            load8<ODT>(g.z + at, z);
+            with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i / 4][i % 4] *= act_slope<decltype(act_c)::value>(z[i / 4][i % 4]);
+            });
+        }
+        store8<ODT>((uint16_t *)g.C + at, v);
+    } else if (g.flags & GF_F32) {
+        f32x4 *const p = reinterpret_cast<f32x4 *>((float *)g.C + at);
+        const bool add = (g.flags & GF_ADD) != 0;
+        p[0] = add ? p[0] + v[0] : v[0];
+        p[1] = add ? p[1] + v[1] : v[1];
+    } else {
+        store8<ODT>((uint16_t *)g.C + at, v);
+    }
+}
+
 // ------------------------------------------------------------------- MX4 ----
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));

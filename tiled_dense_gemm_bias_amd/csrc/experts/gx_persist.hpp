@@ -528,6 +528,16 @@ grouped_persist_kernel(Group g) {
                 asm volatile("" : "=v"(v) : "0"(acc[fn][fm]));
                 return v;
             };
+            // Rows of whole 128-byte lines leave non-temporally; others share lines with
+            // the tile's next stores, and are left to the L2 to join (a weight
+            // gradient of 504 columns: 38 us non-temporally).
+            const bool lines = N % 64 == 0;
+            auto store16 = [&](char *at, const u32x4 &v) __attribute__((always_inline)) {
+                if (lines)
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(at));
+                else
+                    *reinterpret_cast<u32x4 *>(at) = v;
+            };
             constexpr int NG = 2 * FM;
             // The wave's block through two alternating 16 x 64 staging buffers to
             // rows of 128 bytes (see gemm_v5.hpp). A: activation applied; SLOPED: times act'(z).
@@ -599,7 +609,7 @@ grouped_persist_kernel(Group g) {
                                     const u32x4 z = *reinterpret_cast<const u32x4 *>(sb + (8 * j + rr) * 128 + ((rc ^ (rr & 7)) * 16));
                                     if (masked && (fm * BD + 8 * j + rr >= rows_left || fh * 64 + rc * 8 >= cols_left)) continue;
                                     const uint32_t offs = st_off + (uint32_t)(2 * fm + j) * pitch8 + (uint32_t)(fh * 128);
-                                    __builtin_nontemporal_store(z, reinterpret_cast<u32x4 *>(Pw + offs));
+                                    store16(Pw + offs, z);
                                 }
                             }
                         }
@@ -625,7 +635,7 @@ grouped_persist_kernel(Group g) {
                         for (int j = 0; j < 2; ++j) {
                             if (masked && (fm * BD + 8 * j + rr >= rows_left || fh * 64 + rc * 8 >= cols_left)) continue;
                             const uint32_t offs = st_off + (uint32_t)(2 * fm + j) * pitch8 + (uint32_t)(fh * 128);
-                            __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4 *>(Cw + offs));
+                            store16(Cw + offs, v[j]);
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);

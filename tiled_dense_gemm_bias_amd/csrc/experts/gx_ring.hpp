@@ -266,63 +266,14 @@ grouped_ring_kernel(Group g) {
             f(v, (crow + m0 + r) * (size_t)N + n);
         }
     };
-    auto eight = [](const uint16_t *p, f32x4 (&v)[2]) __attribute__((always_inline)) {
-        const u32x4 x = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i / 2][2 * (i % 2)] = to_f32<ODT>(x[i] & 0xffffu);
-            v[i / 2][2 * (i % 2) + 1] = to_f32<ODT>(x[i] >> 16);
-        }
-    };
-    auto store8 = [](uint16_t *p, const f32x4 (&v)[2]) __attribute__((always_inline)) {
-        const u32x4 x = {pack2<ODT>(v[0][0], v[0][1]), pack2<ODT>(v[0][2], v[0][3]),
-                         pack2<ODT>(v[1][0], v[1][1]), pack2<ODT>(v[1][2], v[1][3])};
-        __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(p));
-    };
     if constexpr (EPI == EPI_PART) {
         float *const P = g.part + (size_t)split * (TA ? (size_t)g.E * M : (size_t)g.T) * N;
         each([&](f32x4 (&v)[2], size_t at) {
             *reinterpret_cast<f32x4 *>(P + at) = v[0];
             *reinterpret_cast<f32x4 *>(P + at + 4) = v[1];
         });
-    } else if constexpr (EPI == EPI_ACT) {
-        f32x4 bias[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-        if (g.bias && n < N) eight(g.bias + (size_t)e * N + n, bias);
-        with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
-            constexpr int ACT = decltype(act_c)::value;
-            each([&](f32x4 (&v)[2], size_t at) {
-                v[0] += bias[0];
-                v[1] += bias[1];
-                if (g.zout) store8(g.zout + at, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = act_fn<ACT>(v[i / 4][i % 4]);
-                store8((uint16_t *)g.C + at, v);
-            });
-        });
-    } else if constexpr (EPI == EPI_SLOPE) {
-        with_act(g.act, [&](auto act_c) __attribute__((always_inline)) {
-            constexpr int ACT = decltype(act_c)::value;
-            each([&](f32x4 (&v)[2], size_t at) {
-                if constexpr (ACT != ACT_NONE) {
-                    f32x4 z[2];
-                    eight(g.z + at, z);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i / 4][i % 4] *= act_slope<ACT>(z[i / 4][i % 4]);
-                }
-                store8((uint16_t *)g.C + at, v);
-            });
-        });
     } else {
-        if (g.flags & GF_F32) {
-            each([&](f32x4 (&v)[2], size_t at) {
-                f32x4 *const p = reinterpret_cast<f32x4 *>((float *)g.C + at);
-                const bool add = (g.flags & GF_ADD) != 0;
-                p[0] = add ? p[0] + v[0] : v[0];
-                p[1] = add ? p[1] + v[1] : v[1];
-            });
-        } else {
-            each([&](f32x4 (&v)[2], size_t at) { store8((uint16_t *)g.C + at, v); });
-        }
+        each([&](f32x4 (&v)[2], size_t at) { finish<EPI, ODT>(g, v, e, n, at); });
     }
 }
 

@@ -1,3 +1,4 @@
 #include "gx_launch.hpp"
 
-GBX_RING_WGRAD_TABLE(wgrad_tn)
+GBX_GRAD_TABLE(wgrad_tn, EPI_GRAD)
+GBX_GRAD_TABLE(part_tn, EPI_PART)
