@@ -9,15 +9,24 @@
 namespace gbx {
 
 using LaunchFn = hipError_t (*)(Group, hipStream_t);
-enum { TILE_16x64 = 0, TILE_64x64 = 1, TILE_128x128 = 2, kTiles = 3 };
 
-// [operand type: f16, bf16][tile]
-extern const LaunchFn fwd_nt[2][kTiles];      // B [N][K]
-extern const LaunchFn fwd_nn[2][kTiles];      // B [K][N]
-extern const LaunchFn slope_nt[2][kTiles];
-extern const LaunchFn slope_nn[2][kTiles];
-extern const LaunchFn wgrad_tn[2][kTiles];    // no 16x64 tile: At's swizzle needs 64 rows
-extern const LaunchFn mx4_nt[2][kTiles];      // [output type]
+// Ring kernel tiles: X(columns of the table, BM, BN, WM, WN, STAGES). The stages
+// are what lets two to four workgroups share a CU.
+#define GBX_TILES(X, ...)                                                                       \
+    X(16, 64, 1, 4, 4, __VA_ARGS__) X(32, 64, 1, 4, 4, __VA_ARGS__) X(64, 64, 2, 2, 3, __VA_ARGS__) \
+    X(64, 128, 2, 2, 3, __VA_ARGS__) X(128, 64, 2, 2, 2, __VA_ARGS__) X(128, 128, 2, 2, 2, __VA_ARGS__)
+enum { TILE_16x64, TILE_32x64, TILE_64x64, TILE_64x128, TILE_128x64, TILE_128x128, kTiles };
+// Weight gradients (At's swizzle needs 64 rows).
+#define GBX_GRAD_TILES(X, ...) X(64, 64, 2, 2, 4, __VA_ARGS__) X(128, 128, 2, 2, 2, __VA_ARGS__)
+enum { GRAD_64x64, GRAD_128x128, kGradTiles };
+
+// [operand type: f16, bf16][tile]; part_*: partial sums of a split.
+extern const LaunchFn fwd_nt[2][kTiles], part_nt[2][kTiles];      // B [N][K]
+extern const LaunchFn fwd_nn[2][kTiles], part_nn[2][kTiles];      // B [K][N]
+extern const LaunchFn slope_nt[2][kTiles], slope_nn[2][kTiles];
+extern const LaunchFn wgrad_tn[2][kGradTiles], part_tn[2][kGradTiles];
+extern const LaunchFn mx4_nt[2][kTiles];                          // [output type]
+extern const LaunchFn part_mx4[2][kTiles];                        // both the same
 
 // Persistent 256 x 256 kernels: [act], one table an operand type.
 extern const LaunchFn big_fwd_nt_f16[kNumActs], big_fwd_nt_bf16[kNumActs];
@@ -29,39 +38,23 @@ extern const LaunchFn big_wgrad_tn[2][2];   // [operand type][GRAD_16, GRAD_F32]
 
 }  // namespace gbx
 
-#define GBX_RING_KERNEL_(...) template __global__ void gbx::grouped_ring_kernel<__VA_ARGS__>(gbx::Group);
+#define GBX_KERNEL_(BM, BN, WM, WN, ST, OP, DT, EPI, TB, TA) \
+    template __global__ void gbx::grouped_ring_kernel<BM, BN, WM, WN, ST, OP, DT, gbx::EPI, TB, TA>(gbx::Group);
+#define GBX_LAUNCH_(BM, BN, WM, WN, ST, OP, DT, EPI, TB, TA) gbx::launch_ring<BM, BN, WM, WN, ST, OP, DT, gbx::EPI, TB, TA>,
 #ifdef __HIP_DEVICE_COMPILE__
-#define GBX_RING_TABLE_(NAME, O0, O1, T0, T1, EPI, TB)                                          \
-    GBX_RING_KERNEL_(16, 64, 1, 4, 4, O0, T0, EPI, TB, false)                                   \
-    GBX_RING_KERNEL_(64, 64, 2, 2, 4, O0, T0, EPI, TB, false)                                   \
-    GBX_RING_KERNEL_(128, 128, 2, 2, 2, O0, T0, EPI, TB, false)                                 \
-    GBX_RING_KERNEL_(16, 64, 1, 4, 4, O1, T1, EPI, TB, false)                                   \
-    GBX_RING_KERNEL_(64, 64, 2, 2, 4, O1, T1, EPI, TB, false)                                   \
-    GBX_RING_KERNEL_(128, 128, 2, 2, 2, O1, T1, EPI, TB, false)
-#define GBX_RING_WGRAD_TABLE(NAME)                                                              \
-    GBX_RING_KERNEL_(64, 64, 2, 2, 4, 0, 0, gbx::EPI_GRAD, false, true)                         \
-    GBX_RING_KERNEL_(128, 128, 2, 2, 2, 0, 0, gbx::EPI_GRAD, false, true)                       \
-    GBX_RING_KERNEL_(64, 64, 2, 2, 4, 1, 1, gbx::EPI_GRAD, false, true)                         \
-    GBX_RING_KERNEL_(128, 128, 2, 2, 2, 1, 1, gbx::EPI_GRAD, false, true)
+#define GBX_TABLE_(NAME, N, TILES, O0, O1, T0, T1, ...) TILES(GBX_KERNEL_, O0, T0, __VA_ARGS__) TILES(GBX_KERNEL_, O1, T1, __VA_ARGS__)
+#define GBX_MX4_PART_TABLE(NAME) GBX_TILES(GBX_KERNEL_, 2, 0, EPI_PART, true, false)
 #else
-#define GBX_RING_TABLE_(NAME, O0, O1, T0, T1, EPI, TB)                                          \
-    const gbx::LaunchFn gbx::NAME[2][gbx::kTiles] = {                                           \
-        {gbx::launch_ring<16, 64, 1, 4, 4, O0, T0, EPI, TB, false>,                             \
-         gbx::launch_ring<64, 64, 2, 2, 4, O0, T0, EPI, TB, false>,                             \
-         gbx::launch_ring<128, 128, 2, 2, 2, O0, T0, EPI, TB, false>},                          \
-        {gbx::launch_ring<16, 64, 1, 4, 4, O1, T1, EPI, TB, false>,                             \
-         gbx::launch_ring<64, 64, 2, 2, 4, O1, T1, EPI, TB, false>,                             \
-         gbx::launch_ring<128, 128, 2, 2, 2, O1, T1, EPI, TB, false>}};
-#define GBX_RING_WGRAD_TABLE(NAME)                                                              \
-    const gbx::LaunchFn gbx::NAME[2][gbx::kTiles] = {                                           \
-        {nullptr, gbx::launch_ring<64, 64, 2, 2, 4, 0, 0, gbx::EPI_GRAD, false, true>,          \
-         gbx::launch_ring<128, 128, 2, 2, 2, 0, 0, gbx::EPI_GRAD, false, true>},                \
-        {nullptr, gbx::launch_ring<64, 64, 2, 2, 4, 1, 1, gbx::EPI_GRAD, false, true>,          \
-         gbx::launch_ring<128, 128, 2, 2, 2, 1, 1, gbx::EPI_GRAD, false, true>}};
+#define GBX_TABLE_(NAME, N, TILES, O0, O1, T0, T1, ...) \
+    const gbx::LaunchFn gbx::NAME[2][gbx::N] = {{TILES(GBX_LAUNCH_, O0, T0, __VA_ARGS__)}, {TILES(GBX_LAUNCH_, O1, T1, __VA_ARGS__)}};
+#define GBX_MX4_PART_TABLE(NAME)                                                                \
+    const gbx::LaunchFn gbx::NAME[2][gbx::kTiles] = {{GBX_TILES(GBX_LAUNCH_, 2, 0, EPI_PART, true, false)}, \
+                                                     {GBX_TILES(GBX_LAUNCH_, 2, 0, EPI_PART, true, false)}};
 #endif
-// 16-bit operands (the output's type is theirs), or 4-bit ones with each output type.
-#define GBX_RING_TABLE(NAME, EPI, TB) GBX_RING_TABLE_(NAME, 0, 1, 0, 1, gbx::EPI, TB)
-#define GBX_RING_MX4_TABLE(NAME) GBX_RING_TABLE_(NAME, 2, 2, 0, 1, gbx::EPI_ACT, true)
+// 16-bit operands (the output's type is theirs), weight gradients, 4-bit operands with each output type.
+#define GBX_RING_TABLE(NAME, EPI, TB) GBX_TABLE_(NAME, kTiles, GBX_TILES, 0, 1, 0, 1, EPI, TB, false)
+#define GBX_GRAD_TABLE(NAME, EPI) GBX_TABLE_(NAME, kGradTiles, GBX_GRAD_TILES, 0, 1, 0, 1, EPI, false, true)
+#define GBX_MX4_TABLE(NAME) GBX_TABLE_(NAME, kTiles, GBX_TILES, 2, 2, 0, 1, EPI_ACT, true, false)
 
 #define GBX_BIG_KERNEL_(...) template __global__ void gbx::grouped_persist_kernel<__VA_ARGS__>(gbx::Group);
 #ifdef __HIP_DEVICE_COMPILE__
