@@ -98,6 +98,7 @@ size_t size3(int64_t a, int64_t b, int64_t c) { return (size_t)a * (size_t)b * (
 // The ring kernel of a plan, then (a split) the second pass.
 int launch_split(gbx::Group &g, const gbx::Plan &p, const gbx::LaunchFn &whole, const gbx::LaunchFn &part,
                  const gbx::LaunchFn &reduce, void *workspace) {
+    if (p.stream) g.flags |= gbx::GF_STREAM;
     if (p.splits == 1) return hip_result(whole(g, t_stream));
     g.splits = p.splits;
     g.part = (float *)workspace;

@@ -40,7 +40,8 @@ struct Group {
     int act, flags, splits;
     int row_bound;               // rows mode: most row tiles the grid was made for
 };
-enum { GF_F32 = 1, GF_ADD = 2 };   // EPI_GRAD: fp32 output, added to what is there
+// EPI_GRAD: fp32 output, added to what is there; B read once and too large to stay in the caches.
+enum { GF_F32 = 1, GF_ADD = 2, GF_STREAM = 4 };
 
 __device__ __forceinline__ int clamp_row(int v, int T) { return min(max(v, 0), T); }
 
@@ -104,14 +105,24 @@ inline long long row_tile_bound(long long T, long long E, int bm) {
     return T / bm + (E < T ? E : T);
 }
 
-// The expert that row tile number t (in expert order, t < total_row_tiles) lies
-// in, with the number of row tiles before it, its tiles, rows and first row. Every lane gets
-// the same answer.
+// The expert that row tile number t (in expert order) lies in, with the number of
+// row tiles before it, its tiles, rows and first row; `total` is that of total_row_tiles, and the
+// rest is set where t < total. Every lane gets the same answer.
 struct Found {
-    int e, before, tiles, start, rows;
+    int e, before, tiles, start, rows, total;
 };
+__device__ __forceinline__ Found found_at(int e0, unsigned long long past, int before, int upto, int n, int start, int rows) {
+    const int l = __builtin_amdgcn_readfirstlane(__ffsll(past) - 1);
+    Found f;
+    f.e = e0 + l;
+    f.tiles = __builtin_amdgcn_readlane(n, l);
+    f.before = before + __builtin_amdgcn_readlane(upto, l) - f.tiles;
+    f.start = __builtin_amdgcn_readlane(start, l);
+    f.rows = __builtin_amdgcn_readlane(rows, l);
+    return f;
+}
 __device__ __forceinline__ Found find_row_tile(const Group &g, int bm, int t, int lane) {
-    Found f = {0, 0, 0, 0, 0};
+    Found f = {0, 0, 0, 0, 0, 0};
     int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) {
         int n = 0, start = 0, rows = 0;
@@ -122,21 +133,33 @@ __device__ __forceinline__ Found find_row_tile(const Group &g, int bm, int t, in
         const int upto = wave_scan(n, lane);
         const unsigned long long past = __ballot(before + upto > t);
         if (past) {
-            const int l = __ffsll(past) - 1;
-            f.e = e0 + l;
-            f.tiles = __shfl(n, l);
-            f.before = before + __shfl(upto, l) - f.tiles;
-            f.start = __shfl(start, l);
-            f.rows = __shfl(rows, l);
+            f = found_at(e0, past, before, upto, n, start, rows);
             break;
         }
-        before += __shfl(upto, 63);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
-    f.e = __builtin_amdgcn_readfirstlane(f.e);
-    f.before = __builtin_amdgcn_readfirstlane(f.before);
-    f.tiles = __builtin_amdgcn_readfirstlane(f.tiles);
-    f.start = __builtin_amdgcn_readfirstlane(f.start);
-    f.rows = __builtin_amdgcn_readfirstlane(f.rows);
+    return f;
+}
+
+// For up to 64 experts, one reading of the offsets for both the total and the
+// tile: `tile_of(total)` gives the row tile wanted, or -1.
+template <class F>
+__device__ __forceinline__ Found locate_few(const Group &g, int bm, int lane, F &&tile_of) {
+    int n = 0, start = 0, rows = 0;
+    if (lane < g.E) {
+        expert_rows(g, lane, start, rows);
+        n = ceil_div(rows, bm);
+    }
+    const int upto = wave_scan(n, lane);
+    // (Up to 64 experts of up to 2^31 / 16 row tiles overflow only for offsets that decrease.)
+    const int total = min((int)min((unsigned)__builtin_amdgcn_readlane(upto, 63), 0x7fffffffu), g.row_bound);
+    const int t = tile_of(total);
+    Found f = {0, 0, 0, 0, 0, total};
+    const unsigned long long past = __ballot(upto > t);
+    if (t >= 0 && past) {
+        f = found_at(0, past, 0, upto, n, start, rows);
+        f.total = total;
+    }
     return f;
 }
 

@@ -27,6 +27,7 @@ struct Plan {
     bool big;       // persistent 256 x 256 kernel
     int tile;       // ring kernel's tile otherwise
     int splits;
+    bool stream;    // B is read non-temporally
 };
 
 inline double ring_cost(const TileCost &t, double tiles, double slices, double cus) {
@@ -57,7 +58,7 @@ inline double row_tiles(double T, double E, int bm) {
 // Rows mode: T rows, `cols` columns, a depth of `words` 16-bit words.
 inline Plan plan_rows(int64_t T, int64_t E, int64_t cols, int64_t words, size_t workspace, int cus) {
     const double slices = ceil(words / 64.0);
-    Plan best = {false, TILE_16x64, 1};
+    Plan best = {false, TILE_16x64, 1, false};
     double least = 1e300;
     for (int i = 0; i < kTiles; ++i) {
         const TileCost &t = kRowTiles[i];
@@ -67,19 +68,32 @@ inline Plan plan_rows(int64_t T, int64_t E, int64_t cols, int64_t words, size_t 
             const double c = ring_cost(t, tiles * s, ceil(slices / s), cus) + (s > 1 ? reduce_cost((double)T * cols, s) : 0);
             if (c < least) {
                 least = c;
-                best = {false, i, s};
+                best = {false, i, s, false};
             }
         }
     }
     // The persistent kernel's stream needs two slices.
-    if (slices >= 2 && big_cost(row_tiles(T, E, 256) * ceil(cols / 256.0), slices, cus) < least) best = {true, 0, 1};
+    if (slices >= 2 && big_cost(row_tiles(T, E, 256) * ceil(cols / 256.0), slices, cus) < least) best = {true, 0, 1, false};
+    // B read once (about one row tile an expert), and too large for the 256 MiB
+    // cache behind the L2 to hold until the next call: read non-temporally (12 of
+    // 32 experts of 2816 x 2048 bf16, 16 rows: 36 -> 32 us; a B that the cache
+    // holds is 10 to 25 % slower so). Few tiles are then split in four, so that more of
+    // them read at once (32 -> 28 us; 2048 tiles: 60 us whole, 71 split; 22 slices: 28 and 36).
+    const double some = E < T ? E : T, b_bytes = 2.0 * E * cols * words;
+    const TileCost &t = kRowTiles[best.tile];
+    if (!best.big && t.bm <= 64 && T / some <= t.bm && b_bytes > 128.0 * 1024 * 1024) {
+        best.stream = true;
+        const double tiles = row_tiles(T, E, t.bm) * ceil((double)cols / t.bn);
+        if (t.bm <= 32 && best.splits == 1 && tiles <= 5.0 * cus && slices >= 32 && 16.0 * T * cols <= (double)workspace)
+            best.splits = 4;
+    }
     return best;
 }
 
 // Weight gradients: E products of M x N, summed over T / E rows on average.
 inline Plan plan_grad(int64_t T, int64_t E, int64_t M, int64_t N, size_t workspace, int cus) {
     const double slices = ceil((double)T / E / 64.0);
-    Plan best = {false, GRAD_64x64, 1};
+    Plan best = {false, GRAD_64x64, 1, false};
     double least = 1e300;
     for (int i = 0; i < kGradTiles; ++i) {
         const TileCost &t = kGradTileCost[i];
@@ -89,12 +103,12 @@ inline Plan plan_grad(int64_t T, int64_t E, int64_t M, int64_t N, size_t workspa
             const double c = ring_cost(t, tiles * s, ceil(slices / s), cus) + (s > 1 ? reduce_cost((double)E * M * N, s) : 0);
             if (c < least) {
                 least = c;
-                best = {false, i, s};
+                best = {false, i, s, false};
             }
         }
     }
     const double tiles = (double)E * ceil(M / 256.0) * ceil(N / 256.0);
-    if (big_cost(tiles, slices < 2 ? 2 : slices, cus) < least) best = {true, 0, 1};
+    if (big_cost(tiles, slices < 2 ? 2 : slices, cus) < least) best = {true, 0, 1, false};
     return best;
 }
 

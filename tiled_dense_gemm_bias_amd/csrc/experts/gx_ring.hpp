@@ -18,6 +18,17 @@
 
 namespace gbx {
 
+// buffer_load_lds16 (gba_dma.hpp), non-temporal.
+__device__ __forceinline__ void buffer_load_lds16_nt(__amdgpu_buffer_rsrc_t rsrc, uint32_t voffset, uint32_t lds_base) {
+    asm volatile(
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %0, %1, 0 offen nt lds"
+        :
+        : "v"(voffset), "s"(rsrc), "s"(lds_base)
+        : "memory", "m0");
+}
+
 template <int BM, int BN, int WM, int WN, int STAGES, int OP, int ODT, int EPI, bool TB, bool TA>
 __global__ void __launch_bounds__(256)
 grouped_ring_kernel(Group g) {
@@ -49,31 +60,48 @@ grouped_ring_kernel(Group g) {
 
     // ---- the work unit: expert, tile, K range ----
     const int tiles_n = ceil_div(g.N, BN);
-    int e, start, rows, m0, n0, split;
+    int e, start, rows, m0, n0, split = 0;
     {
-        const int row_tiles = TA ? 0 : total_row_tiles(g, BM, lane);
-        const int tiles_m = ceil_div(g.M, BM);   // TA
-        const long long tiles = TA ? (long long)g.E * tiles_m * tiles_n : (long long)row_tiles * tiles_n;
-        const long long units = tiles * g.splits;
         const long long b = (long long)blockIdx.y * gridDim.x + blockIdx.x;
-        if (b >= units) return;
-        int u = xcd_remap((int)b, (int)units);
-        split = u / (int)tiles;
-        u -= split * (int)tiles;
+        // This workgroup's tile among `tiles` (split-major units, one contiguous range an XCD), or -1.
+        auto my_tile = [&](long long tiles) __attribute__((always_inline)) {
+            const long long units = tiles * g.splits;
+            if (b >= units) return -1;
+            const int u = xcd_remap((int)b, (int)units);
+            split = u / (int)tiles;
+            return u - split * (int)tiles;
+        };
         int tm, tn;
         if constexpr (TA) {
+            const int tiles_m = ceil_div(g.M, BM);
+            const int u = my_tile((long long)g.E * tiles_m * tiles_n);
+            if (u < 0) return;
             e = u / (tiles_m * tiles_n);
             grouped_tile(u - e * tiles_m * tiles_n, tiles_m, tiles_n, 4, tm, tn);
-            expert_rows(g, e, start, rows);
+            expert_rows_uniform(g, e, start, rows);
         } else {
-            const Found f = find_row_tile(g, BM, u / tiles_n, lane);
+            int u = -1;
+            Found f;
+            if (g.E <= 64) {
+                f = locate_few(g, BM, lane, [&](int total) __attribute__((always_inline)) {
+                    u = my_tile((long long)total * tiles_n);
+                    return u < 0 ? -1 : u / tiles_n;
+                });
+                if (u < 0) return;
+            } else {
+                u = my_tile((long long)total_row_tiles(g, BM, lane) * tiles_n);
+                if (u < 0) return;
+                f = find_row_tile(g, BM, u / tiles_n, lane);
+            }
             e = f.e;
             start = f.start;
             rows = f.rows;
-            grouped_tile(u - f.before * tiles_n, f.tiles, tiles_n, 4, tm, tn);
+            grouped_tile(u - f.before * tiles_n, max(f.tiles, 1), tiles_n, 4, tm, tn);
         }
         m0 = tm * BM;
         n0 = tn * BN;
+        // Offsets that decrease could name a tile past its expert's rows.
+        if (!TA && (m0 < 0 || m0 >= rows || n0 < 0)) return;
     }
     const int K = TA ? rows : g.K;          // depth of the sum
     const int M = TA ? g.M : rows;          // rows of the expert's output
@@ -113,11 +141,18 @@ grouped_ring_kernel(Group g) {
         }
     }
     const uint32_t smem_lds = (uint32_t)(uintptr_t)(GBA_LDS void *)smem;
+    const bool stream = (g.flags & GF_STREAM) != 0;
+    auto load_b = [&](__amdgpu_buffer_rsrc_t rsrc, uint32_t voffset, uint32_t dst) __attribute__((always_inline)) {
+        if (BM <= 64 && stream)
+            buffer_load_lds16_nt(rsrc, voffset, dst);
+        else
+            buffer_load_lds16(rsrc, voffset, dst);
+    };
     // Slice kt (of this unit) into stage `stage`; a slice past the last reads
     // nothing and lands zeros, which keeps the wait counts uniform.
     auto load_slice = [&](int kt, int stage) __attribute__((always_inline)) {
         const bool live = kt < nk;
-        const int k0 = (kt0 + (live ? kt : 0)) * BK;
+        const int slice = kt0 + (live ? kt : 0), k0 = slice * BK;
         const uint32_t kin = live ? (uint32_t)min(K - k0, BK) : 0u;
         const bool in_k = (uint32_t)ca * 8u < kin;   // K-contiguous tiles: chunk inside K
         const uint32_t base = smem_lds + (uint32_t)(stage * STAGE);
@@ -133,12 +168,11 @@ grouped_ring_kernel(Group g) {
             buffer_load_lds16(ra, TA || in_k ? off[i] : kOobOffset, wave_a + (uint32_t)(i * NT * 16));
 #pragma unroll
         for (int i = 0; i < B_LD; ++i)
-            buffer_load_lds16(rb, !TB || in_k ? off[A_LD + i] : kOobOffset,
-                              base + (uint32_t)(A_BYTES + wid * 1024 + i * NT * 16));
+            load_b(rb, !TB || in_k ? off[A_LD + i] : kOobOffset, base + (uint32_t)(A_BYTES + wid * 1024 + i * NT * 16));
         if constexpr (MX) {
             // Wave w loads plane w % 2 of A's (w < 2) or B's scales: four rows'
             // dwords a lane (range checks are per dword), lanes past the tile nothing.
-            const int plane = 2 * (kt0 + kt) + (wid & 1);
+            const int plane = 2 * slice + (wid & 1);
             const bool there = live && plane * 32 < K;   // 32 words: 128 values a plane
             const bool of_a = wid < 2;
             const size_t all = of_a ? (size_t)g.T : (size_t)g.E * N;
