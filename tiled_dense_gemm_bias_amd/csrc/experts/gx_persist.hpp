@@ -95,16 +95,19 @@ grouped_persist_kernel(Group g) {
     const uint32_t smem_lds = (uint32_t)(uintptr_t)(GBA_LDS void *)smem;
     const int tiles_n = ceil_div(N, BN), tiles_m_ta = TA ? ceil_div(g.M, BM) : 0;
 
-    // Rows mode, up to 64 experts: lane l holds the row tiles of experts 0 .. l.
-    int upto = 0, row_tiles = 0;
-    if constexpr (!TA) {
-        row_tiles = total_row_tiles(g, BM, lane_now());
-        if (g.E <= 64) {
-            const int l = lane_now();
-            int start = 0, rows = 0;
-            if (l < g.E) expert_rows(g, l, start, rows);
-            upto = wave_scan(ceil_div(rows, BM), l);
+    // Up to 64 experts: lane l holds the first row and the rows of expert l, and (rows
+    // mode) the row tiles of experts 0 .. l, so that a tile's expert costs no memory access.
+    int upto = 0, row_tiles = 0, start_l = 0, rows_l = 0;
+    const bool few = g.E <= 64;
+    if (few) {
+        const int l = lane_now();
+        if (l < g.E) expert_rows(g, l, start_l, rows_l);
+        if constexpr (!TA) {
+            upto = wave_scan(ceil_div(rows_l, BM), l);
+            row_tiles = min(__builtin_amdgcn_readlane(upto, 63), g.row_bound);
         }
+    } else if constexpr (!TA) {
+        row_tiles = total_row_tiles(g, BM, lane_now());
     }
     const int T = TA ? g.E * tiles_m_ta * tiles_n : row_tiles * tiles_n;
     const int G = min((int)gridDim.x, T);
@@ -122,18 +125,24 @@ grouped_persist_kernel(Group g) {
         if constexpr (TA) {
             t.e = idx / (tiles_m_ta * tiles_n);
             grouped_tile(idx - t.e * tiles_m_ta * tiles_n, tiles_m_ta, tiles_n, 4, tm, tn);
-            expert_rows_uniform(g, t.e, t.start, t.klen);
+            if (few) {
+                t.start = __builtin_amdgcn_readlane(start_l, t.e);
+                t.klen = __builtin_amdgcn_readlane(rows_l, t.e);
+            } else {
+                expert_rows_uniform(g, t.e, t.start, t.klen);
+            }
             t.rows = g.M;
             t.nk = max(ceil_div(t.klen, BK), 2);
         } else {
             const int rt = idx / tiles_n;
             int before, tiles;
-            if (g.E <= 64) {
+            if (few) {
                 const unsigned long long past = __ballot(upto > rt);
                 t.e = __builtin_amdgcn_readfirstlane(__ffsll(past) - 1);
                 before = t.e > 0 ? __builtin_amdgcn_readlane(upto, t.e - 1) : 0;
                 tiles = __builtin_amdgcn_readlane(upto, t.e) - before;
-                expert_rows_uniform(g, t.e, t.start, t.rows);
+                t.start = __builtin_amdgcn_readlane(start_l, t.e);
+                t.rows = __builtin_amdgcn_readlane(rows_l, t.e);
             } else {
                 const Found f = find_row_tile(g, BM, rt, lane_now());
                 t.e = f.e;
@@ -532,11 +541,14 @@ grouped_persist_kernel(Group g) {
             // the tile's next stores, and are left to the L2 to join (a weight
             // gradient of 504 columns: 38 us non-temporally).
             const bool lines = N % 64 == 0;
-            auto store16 = [&](char *at, const u32x4 &v) __attribute__((always_inline)) {
+            // (Buffer stores: the compiler joins a non-temporal and an ordinary store of
+            // the same value into an ordinary one, and the outputs then push the inputs
+            // out of the cache behind the L2: 16384 x 8192 x 4096 711 -> 769 us.)
+            auto store16 = [&](__amdgpu_buffer_rsrc_t out, uint32_t at, const u32x4 &v) __attribute__((always_inline)) {
                 if (lines)
-                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(at));
+                    __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)at, 0, 2 /* nt */);
                 else
-                    *reinterpret_cast<u32x4 *>(at) = v;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)at, 0, 0);
             };
             constexpr int NG = 2 * FM;
             // The wave's block through two alternating 16 x 64 staging buffers to
@@ -546,8 +558,10 @@ grouped_persist_kernel(Group g) {
                 constexpr int A = decltype(a_c)::value;
                 constexpr int ZB = 2;
                 constexpr bool SLOPED = EPI == EPI_SLOPE && ACT != ACT_NONE;
-                char *const Cw = reinterpret_cast<char *>((uint16_t *)ga->C + corner);
-                char *const Pw = BIASED && !MX && ga->zout ? reinterpret_cast<char *>(ga->zout + corner) : nullptr;
+                // 128 rows of at most 2^24 bytes: offsets below 2^31.
+                const __amdgpu_buffer_rsrc_t Cw = make_rsrc((uint16_t *)ga->C + corner, 0x7fffffffu);
+                const bool with_z = BIASED && !MX && ga->zout != nullptr;
+                const __amdgpu_buffer_rsrc_t Pw = make_rsrc(with_z ? ga->zout + corner : nullptr, with_z ? 0x7fffffffu : 0u);
                 f32x4 bq[4];
                 u32x2 zq[SLOPED ? ZB : 1][4];
 #pragma unroll
@@ -600,7 +614,7 @@ grouped_persist_kernel(Group g) {
                         if constexpr (BIASED && !MX) {
                             // The pre-activation goes through the same buffer first (a wave's
                             // LDS instructions run in order).
-                            if (Pw) {
+                            if (with_z) {
 #pragma unroll
                                 for (int f = 0; f < 4; ++f)
                                     *staged(f) = u32x2{pack2<ODT>(s[f][0], s[f][1]), pack2<ODT>(s[f][2], s[f][3])};
@@ -609,7 +623,7 @@ grouped_persist_kernel(Group g) {
                                     const u32x4 z = *reinterpret_cast<const u32x4 *>(sb + (8 * j + rr) * 128 + ((rc ^ (rr & 7)) * 16));
                                     if (masked && (fm * BD + 8 * j + rr >= rows_left || fh * 64 + rc * 8 >= cols_left)) continue;
                                     const uint32_t offs = st_off + (uint32_t)(2 * fm + j) * pitch8 + (uint32_t)(fh * 128);
-                                    store16(Pw + offs, z);
+                                    store16(Pw, offs, z);
                                 }
                             }
                         }
@@ -635,7 +649,7 @@ grouped_persist_kernel(Group g) {
                         for (int j = 0; j < 2; ++j) {
                             if (masked && (fm * BD + 8 * j + rr >= rows_left || fh * 64 + rc * 8 >= cols_left)) continue;
                             const uint32_t offs = st_off + (uint32_t)(2 * fm + j) * pitch8 + (uint32_t)(fh * 128);
-                            store16(Cw + offs, v[j]);
+                            store16(Cw, offs, v[j]);
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);
