@@ -168,7 +168,11 @@ __device__ __forceinline__ Found locate_few(const Group &g, int bm, int lane, F 
 // act'(z) in fp32. relu'(0) = 0; at z = +-inf the limit; NaN for NaN.
 //  sigmoid:   t / (1 + t)^2 with t = e^-|z| (no cancellation on either side).
 //  softplus:  the logistic of z.
-//  gelu:      Phi(z) + z phi(z); Phi as in act_fn (2^Q(|z|) is Phi(-|z|), within 8e-6 of it).
+//  gelu:      Phi(z) + z phi(z) = q for z <= 0 and 1 - q for z > 0, with q =
+//             e^(-z^2/2) P(|z|): P, of degree 7, is fitted to (m(x) - x) / sqrt(2 pi)
+//             with m the Mills ratio Phi(-x) / phi(x)
+//             (tiled_dense_gemm_bias_amd/gelu_slope_fit.py), q within 4.1e-6. |z| is
+//             clamped in P only: at z = +-inf q is 0 and NaN stays NaN.
 //  gelu_tanh: z = tanh form; with s = 1 / (1 + e), e = e^(-2y),
 //             y = sqrt(2/pi) (z + c z^3): s + z s (1 - s) 2 y', and 1 - s = e s.
 //             Outside |z| = 10 the slope is 0 or 1 to 1e-30: z is clamped there,
@@ -185,21 +189,16 @@ __device__ __forceinline__ float act_slope(float z) {
     } else if constexpr (ACT == ACT_SOFTPLUS) {
         return act_fn<ACT_SIGMOID>(z);
     } else if constexpr (ACT == ACT_GELU) {
-        const float az = fminf(fabsf(z), 30.0f);
-        float q = fmaf(az, -1.8348076764596044e-06f, 6.15982135059312e-05f);
-        q = fmaf(az, q, -0.0009305241401307285f);
-        q = fmaf(az, q, 0.008507887832820415f);
-        q = fmaf(az, q, -0.05396006256341934f);
-        q = fmaf(az, q, -0.4584644138813019f);
-        q = fmaf(az, q, -1.1512510776519775f);
-        q = fmaf(az, q, -0.9999952912330627f);
-        const float lower = __builtin_amdgcn_exp2f(q);   // Phi(-|z|)
-        // |z| phi(z), 1 / sqrt(2 pi) = 0.39894228
-        const float zp = az * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * az * az);
-        // z > 0: 1 - lower + zp; z < 0: lower - zp
-        const float d = zp - lower;
-        const float r = z > 0.0f ? 1.0f + d : -d;
-        return z != z ? z : r;
+        const float a = fminf(fabsf(z), 8.0f);
+        float p = fmaf(a, -0.00016855745343491435f, 0.002319070976227522f);
+        p = fmaf(a, p, -0.013923607766628265f);
+        p = fmaf(a, p, 0.049940045922994614f);
+        p = fmaf(a, p, -0.12582695484161377f);
+        p = fmaf(a, p, 0.2479596585035324f);
+        p = fmaf(a, p, -0.7976623773574829f);
+        p = fmaf(a, p, 0.49999603629112244f);
+        const float q = p * __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+        return z > 0.0f ? 1.0f - q : q;
     } else if constexpr (ACT == ACT_GELU_TANH) {
         const float c = fminf(fmaxf(z, -10.0f), 10.0f);
         const float c2 = c * c;

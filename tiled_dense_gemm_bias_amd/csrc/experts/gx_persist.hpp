@@ -563,7 +563,21 @@ grouped_persist_kernel(Group g) {
                 const bool with_z = BIASED && !MX && ga->zout != nullptr;
                 const __amdgpu_buffer_rsrc_t Pw = make_rsrc(with_z ? ga->zout + corner : nullptr, with_z ? 0x7fffffffu : 0u);
                 f32x4 bq[4];
-                u32x2 zq[SLOPED ? ZB : 1][4];
+                u32x2 zq[SLOPED ? 2 : 1][SLOPED ? ZB : 1][4];
+                // z of ZB groups (a lane: one row, four columns), a batch ahead of its use.
+                auto load_z = [&](int batch) __attribute__((always_inline)) {
+                    const char *const Zw = reinterpret_cast<const char *>(ga->z + corner);
+#pragma unroll
+                    for (int b = 0; b < ZB; ++b)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int fh = (batch * ZB + b) / FM, fm = (batch * ZB + b) % FM;
+                            const uint32_t zo = z_off + (uint32_t)fm * 2u * pitch8 + (uint32_t)(fh * 128 + f * 32);
+                            zq[batch & 1][b][f] = !masked || (fm * BD + wr < rows_left && fh * 64 + 16 * f + 4 * wg < cols_left)
+                                                      ? *reinterpret_cast<const u32x2 *>(Zw + zo)
+                                                      : u32x2{0u, 0u};
+                        }
+                };
 #pragma unroll
                 for (int gi = 0; gi <= NG; ++gi) {
                     u32x4 v[2];
@@ -585,20 +599,8 @@ grouped_persist_kernel(Group g) {
                             }
                         }
                         if constexpr (SLOPED) {
-                            // z of ZB row blocks of this column half at once (a lane: one
-                            // row, four columns), so that few loads wait behind stores.
-                            if (gi % ZB == 0) {
-                                const char *const Zw = reinterpret_cast<const char *>(ga->z + corner);
-#pragma unroll
-                                for (int b = 0; b < ZB; ++b)
-#pragma unroll
-                                    for (int f = 0; f < 4; ++f) {
-                                        const uint32_t zo = z_off + (uint32_t)(fm + b) * 2u * pitch8 + (uint32_t)(fh * 128 + f * 32);
-                                        zq[b][f] = !masked || ((fm + b) * BD + wr < rows_left && fh * 64 + 16 * f + 4 * wg < cols_left)
-                                                       ? *reinterpret_cast<const u32x2 *>(Zw + zo)
-                                                       : u32x2{0u, 0u};
-                                    }
-                            }
+                            if (gi == 0) load_z(0);
+                            if (gi % ZB == 0 && gi + ZB < NG) load_z(gi / ZB + 1);
                         }
                         f32x4 s[4];
 #pragma unroll
@@ -631,7 +633,7 @@ grouped_persist_kernel(Group g) {
                         for (int f = 0; f < 4; ++f) {
                             f32x4 a = s[f];
                             if constexpr (SLOPED) {
-                                const u32x2 z = zq[fm % ZB][f];
+                                const u32x2 z = zq[gi / ZB & 1][gi % ZB][f];
                                 a[0] *= act_slope<ACT>(to_f32<ODT>(z.x & 0xffffu));
                                 a[1] *= act_slope<ACT>(to_f32<ODT>(z.x >> 16));
                                 a[2] *= act_slope<ACT>(to_f32<ODT>(z.y & 0xffffu));
