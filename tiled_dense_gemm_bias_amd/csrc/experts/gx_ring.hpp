@@ -30,7 +30,7 @@ __device__ __forceinline__ void buffer_load_lds16_nt(__amdgpu_buffer_rsrc_t rsrc
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, int OP, int ODT, int EPI, bool TB, bool TA>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)   // two workgroups a CU at least
 grouped_ring_kernel(Group g) {
     constexpr int NT = 256, BK = 64;
     constexpr bool MX = OP == OP_MX4;
@@ -148,43 +148,99 @@ grouped_ring_kernel(Group g) {
         else
             buffer_load_lds16(rsrc, voffset, dst);
     };
-    // Slice kt (of this unit) into stage `stage`; a slice past the last reads
-    // nothing and lands zeros, which keeps the wait counts uniform.
-    auto load_slice = [&](int kt, int stage) __attribute__((always_inline)) {
-        const bool live = kt < nk;
-        const int slice = kt0 + (live ? kt : 0), k0 = slice * BK;
-        const uint32_t kin = live ? (uint32_t)min(K - k0, BK) : 0u;
-        const bool in_k = (uint32_t)ca * 8u < kin;   // K-contiguous tiles: chunk inside K
-        const uint32_t base = smem_lds + (uint32_t)(stage * STAGE);
-        const __amdgpu_buffer_rsrc_t ra =
-            TA ? make_rsrc(Ae + (size_t)k0 * M + m0, kin * (uint32_t)M * 2u)
-               : make_rsrc(Ae + (size_t)m0 * K + k0, live ? (uint32_t)rows_a * (uint32_t)K * 2u - (uint32_t)k0 * 2u : 0u);
-        const __amdgpu_buffer_rsrc_t rb =
-            TB ? make_rsrc(Be + (size_t)n0 * K + k0, live ? (uint32_t)rows_b * (uint32_t)K * 2u - (uint32_t)k0 * 2u : 0u)
-               : make_rsrc(Be + (size_t)k0 * N + n0, kin * (uint32_t)N * 2u);
+    // The slice to load next: its corners and byte ranges, carried from slice to
+    // slice. Up to the last slice they move by constants; the last one (K's end:
+    // chunks past it out of range, fewer rows) and those past it (empty ranges: zeros land
+    // and no memory is read, which keeps the wait counts uniform) are formed in
+    // one rarely taken block. Forming every slice from scratch cost a wave that has its
+    // SIMD to itself as long as the slice's matrix work.
+    struct {
+        const uint16_t *pa, *pb;
+        uint32_t na, nb;
+        const uint32_t *ps;   // MX4: this wave's scale plane: w % 2 of A's (w < 2) or B's
+        uint32_t ns;
+        int left;             // slices left to load
+    } pos;
+    const size_t plane_dwords = MX ? (wid < 2 ? (size_t)g.T : (size_t)g.E * N) : 0;
+    auto at_end = [&](int kt) __attribute__((always_inline)) {
+        const int k0 = (kt0 + kt) * BK;
+        const uint32_t kin = pos.left > 0 ? (uint32_t)min(K - k0, BK) : 0u;
+        if constexpr (TA) {
+            pos.na = kin * (uint32_t)M * 2u;
+        } else {
+            if (pos.left <= 0) pos.na = 0;
+#pragma unroll
+            for (int i = 0; i < A_LD; ++i)
+                if ((uint32_t)ca * 8u >= kin) off[i] = kOobOffset;
+        }
+        if constexpr (!TB) {
+            pos.nb = kin * (uint32_t)N * 2u;
+        } else {
+            if (pos.left <= 0) pos.nb = 0;
+#pragma unroll
+            for (int i = 0; i < B_LD; ++i)
+                if ((uint32_t)ca * 8u >= kin) off[A_LD + i] = kOobOffset;
+        }
+        // 32 words: 128 values a plane
+        if (MX && (pos.left <= 0 || (2 * (kt0 + kt) + (wid & 1)) * 32 >= K)) pos.ns = 0;
+    };
+    {
+        const int k0 = kt0 * BK;
+        if constexpr (TA) {
+            pos.pa = Ae + ((size_t)k0 * M + m0);
+            pos.na = (uint32_t)BK * (uint32_t)M * 2u;
+        } else {
+            pos.pa = Ae + ((size_t)m0 * K + k0);
+            pos.na = (uint32_t)rows_a * (uint32_t)K * 2u - (uint32_t)k0 * 2u;
+        }
+        if constexpr (TB) {
+            pos.pb = Be + ((size_t)n0 * K + k0);
+            pos.nb = (uint32_t)rows_b * (uint32_t)K * 2u - (uint32_t)k0 * 2u;
+        } else {
+            pos.pb = Be + ((size_t)k0 * N + n0);
+            pos.nb = (uint32_t)BK * (uint32_t)N * 2u;
+        }
+        pos.left = nk;
+        if constexpr (MX) {
+            pos.ps = (wid < 2 ? g.sa + (size_t)start + m0 : g.sb + (size_t)e * N + n0) +
+                     (size_t)(2 * kt0 + (wid & 1)) * plane_dwords;
+            pos.ns = (uint32_t)(wid < 2 ? rows_a : rows_b) * 4u;
+        }
+    }
+    // Loads the next slice, which is slice kt of this unit, into stage S.
+    auto load_slice = [&](int kt, auto stage_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(stage_c)::value;
+        if (__builtin_expect(pos.left <= 1, 0)) at_end(kt);
+        const uint32_t base = smem_lds + (uint32_t)(S * STAGE);
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(pos.pa, pos.na), rb = make_rsrc(pos.pb, pos.nb);
         const uint32_t wave_a = base + (uint32_t)((wid & (AW - 1)) * 1024);
 #pragma unroll
-        for (int i = 0; i < A_LD; ++i)
-            buffer_load_lds16(ra, TA || in_k ? off[i] : kOobOffset, wave_a + (uint32_t)(i * NT * 16));
+        for (int i = 0; i < A_LD; ++i) buffer_load_lds16(ra, off[i], wave_a + (uint32_t)(i * NT * 16));
 #pragma unroll
         for (int i = 0; i < B_LD; ++i)
-            load_b(rb, !TB || in_k ? off[A_LD + i] : kOobOffset, base + (uint32_t)(A_BYTES + wid * 1024 + i * NT * 16));
+            load_b(rb, off[A_LD + i], base + (uint32_t)(A_BYTES + wid * 1024 + i * NT * 16));
         if constexpr (MX) {
-            // Wave w loads plane w % 2 of A's (w < 2) or B's scales: four rows'
-            // dwords a lane (range checks are per dword), lanes past the tile nothing.
-            const int plane = 2 * slice + (wid & 1);
-            const bool there = live && plane * 32 < K;   // 32 words: 128 values a plane
-            const bool of_a = wid < 2;
-            const size_t all = of_a ? (size_t)g.T : (size_t)g.E * N;
-            const uint32_t *const src = of_a ? g.sa + (size_t)start + m0 : g.sb + (size_t)e * N + n0;
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(src + (there ? (size_t)plane * all : 0),
-                                                        there ? (uint32_t)(of_a ? rows_a : rows_b) * 4u : 0u);
-            const int mine = of_a ? BM : BN;
+            // Four rows' dwords a lane (range checks are per dword); the lanes past
+            // the tile's rows are switched off.
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(pos.ps, pos.ns);
             const uint32_t dst = base + (uint32_t)(A_BYTES + B_BYTES) +
-                                 (of_a ? (uint32_t)((wid & 1) * BM * 4) : (uint32_t)(2 * BM * 4 + (wid & 1) * BN * 4));
-            // The lanes past the tile's rows write nowhere: they are switched off.
-            if (lane * 4 < mine) buffer_load_lds16(rs, (uint32_t)lane * 16u, dst);
+                                 (wid < 2 ? (uint32_t)((wid & 1) * BM * 4) : (uint32_t)(2 * BM * 4 + (wid & 1) * BN * 4));
+            if (lane * 4 < (wid < 2 ? BM : BN)) buffer_load_lds16(rs, (uint32_t)lane * 16u, dst);
+            pos.ps += 2 * plane_dwords;
         }
+        if constexpr (TA) {
+            pos.pa += (size_t)BK * M;
+        } else {
+            pos.pa += BK;
+            pos.na -= 2u * BK;
+        }
+        if constexpr (TB) {
+            pos.pb += BK;
+            pos.nb -= 2u * BK;
+        } else {
+            pos.pb += (size_t)BK * N;
+        }
+        --pos.left;
     };
 
     // ---- fragments ----
@@ -194,78 +250,97 @@ grouped_ring_kernel(Group g) {
     for (int a = 0; a < FN; ++a)
 #pragma unroll
         for (int b = 0; b < FM; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    auto compute = [&](int stage) __attribute__((always_inline)) {
-        const char *const base = smem + stage * STAGE;
+    struct Frags {
+        u32x4 a[FM], b[FN];
+        uint32_t sa[FM], sb[FN];
+    };
+    // Rows along K are gathered by transposing reads of four k rows each.
+    auto gather = [&](const char *tile, int kk, int x, int row_bytes, auto chunks_c) __attribute__((always_inline)) {
+        constexpr int CHUNKS = decltype(chunks_c)::value;
+        i16x4 h[2];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 af[FM], bf[FN];
-            uint32_t saf[FM], sbf[FN];
-#pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                if constexpr (TA) {
-                    i16x4 h[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = kk * 32 + 8 * tg + 4 * i + (tj >> 2);
-                        const int m = wm * WTM + f * 16 + 4 * (tj & 3);
-                        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (GBA_LDS i16x4 *)(base + k * (BM * 2) + (((m >> 3) ^ bswz<CHT>(k)) * 16) + (m & 4) * 2));
-                    }
-                    af[f] = __builtin_bit_cast(u32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                } else {
-                    const int r = wm * WTM + f * 16 + tj;
-                    af[f] = *reinterpret_cast<const u32x4 *>(base + r * 128 + (((4 * kk + tg) ^ (r & 7)) * 16));
-                }
-                if constexpr (MX)
-                    saf[f] = *reinterpret_cast<const uint32_t *>(base + A_BYTES + B_BYTES + kk * BM * 4 +
-                                                                 (wm * WTM + f * 16 + tj) * 4) >> (8 * tg);
-            }
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                if constexpr (TB) {
-                    const int r = wn * WTN + f * 16 + tj;
-                    bf[f] = *reinterpret_cast<const u32x4 *>(base + A_BYTES + r * 128 + (((4 * kk + tg) ^ (r & 7)) * 16));
-                } else {
-                    i16x4 h[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int k = kk * 32 + 8 * tg + 4 * i + (tj >> 2);
-                        const int n = wn * WTN + f * 16 + 4 * (tj & 3);
-                        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (GBA_LDS i16x4 *)(base + A_BYTES + k * (BN * 2) + (((n >> 3) ^ bswz<CHB>(k)) * 16) + (n & 4) * 2));
-                    }
-                    bf[f] = __builtin_bit_cast(u32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                }
-                if constexpr (MX)
-                    sbf[f] = *reinterpret_cast<const uint32_t *>(base + A_BYTES + B_BYTES + 2 * BM * 4 + kk * BN * 4 +
-                                                                 (wn * WTN + f * 16 + tj) * 4) >> (8 * tg);
-            }
-#pragma unroll
-            for (int a = 0; a < FN; ++a)
-#pragma unroll
-                for (int b = 0; b < FM; ++b) {
-                    if constexpr (MX)
-                        acc[a][b] = mfma_mx4(bf[a], af[b], acc[a][b], sbf[a], saf[b]);
-                    else
-                        acc[a][b] = mfma16x16x32<OP>(bf[a], af[b], acc[a][b]);
-                }
+        for (int i = 0; i < 2; ++i) {
+            const int k = kk * 32 + 8 * tg + 4 * i + (tj >> 2);
+            h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (GBA_LDS i16x4 *)(tile + k * row_bytes + (((x >> 3) ^ bswz<CHUNKS>(k)) * 16) + (x & 4) * 2));
         }
+        return __builtin_bit_cast(u32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto read_frags = [&](const char *base, int kk, Frags &f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < FM; ++b) {
+            if constexpr (TA) {
+                f.a[b] = gather(base, kk, wm * WTM + b * 16 + 4 * (tj & 3), BM * 2, std::integral_constant<int, CHT>{});
+            } else {
+                const int r = wm * WTM + b * 16 + tj;
+                f.a[b] = *reinterpret_cast<const u32x4 *>(base + r * 128 + (((4 * kk + tg) ^ (r & 7)) * 16));
+            }
+            if constexpr (MX)
+                f.sa[b] = *reinterpret_cast<const uint32_t *>(base + A_BYTES + B_BYTES + kk * BM * 4 +
+                                                              (wm * WTM + b * 16 + tj) * 4) >> (8 * tg);
+        }
+#pragma unroll
+        for (int a = 0; a < FN; ++a) {
+            if constexpr (TB) {
+                const int r = wn * WTN + a * 16 + tj;
+                f.b[a] = *reinterpret_cast<const u32x4 *>(base + A_BYTES + r * 128 + (((4 * kk + tg) ^ (r & 7)) * 16));
+            } else {
+                f.b[a] = gather(base + A_BYTES, kk, wn * WTN + a * 16 + 4 * (tj & 3), BN * 2,
+                                std::integral_constant<int, CHB>{});
+            }
+            if constexpr (MX)
+                f.sb[a] = *reinterpret_cast<const uint32_t *>(base + A_BYTES + B_BYTES + 2 * BM * 4 + kk * BN * 4 +
+                                                              (wn * WTN + a * 16 + tj) * 4) >> (8 * tg);
+        }
+    };
+    auto multiply = [&](const Frags &f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < FN; ++a)
+#pragma unroll
+            for (int b = 0; b < FM; ++b) {
+                if constexpr (MX)
+                    acc[a][b] = mfma_mx4(f.b[a], f.a[b], acc[a][b], f.sb[a], f.sa[b]);
+                else
+                    acc[a][b] = mfma16x16x32<OP>(f.b[a], f.a[b], acc[a][b]);
+            }
     };
 
     // ---- the slices ----
+    static_for<STAGES - 1>([&](auto s_c) __attribute__((always_inline)) { load_slice(decltype(s_c)::value, s_c); });
+    // Slice kt lies in stage kt % STAGES, a constant in each copy of the loop's body.
+    for (int kb = 0; kb < nk; kb += STAGES) {
+        static_for<STAGES>([&](auto s_c) __attribute__((always_inline)) {
+            constexpr int S = decltype(s_c)::value;
+            if (S == 0 || kb + S < nk) {
+                // Slice kt has landed and this wave's reads of slice kt - 1 are done; then the
+                // same holds for all waves, and slice kt - 1's stage is free.
+                wait_vmcnt_lgkm0<(STAGES - 2) * LD>();
+                block_barrier();
+                const char *const base = smem + S * STAGE;
+                constexpr std::integral_constant<int, (S + STAGES - 1) % STAGES> freed{};
+                // A ring of two stages has its next slice only now to ask for: first of
+                // all. Longer ones ask while their first fragments are on the way (small tiles
+                // 5 to 20 % faster so, 128 x 128 15 % slower).
+                if constexpr (STAGES == 2) {
+                    load_slice(kb + S + 1, freed);
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) load_slice(s, s);
-    int stage = 0;
-    for (int kt = 0; kt < nk; ++kt) {
-        // Slice kt has landed and this wave's reads of slice kt - 1 are done; then
-        // the same holds for all waves, and slice kt - 1's stage is free.
-        wait_vmcnt_lgkm0<(STAGES - 2) * LD>();
-        block_barrier();
-        load_slice(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-        compute(stage);
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+                    for (int kk = 0; kk < 2; ++kk) {
+                        Frags f;
+                        read_frags(base, kk, f);
+                        multiply(f);
+                    }
+                } else {
+                    Frags f0, f1;
+                    read_frags(base, 0, f0);
+                    load_slice(kb + S + STAGES - 1, freed);
+                    read_frags(base, 1, f1);
+                    multiply(f0);
+                    multiply(f1);
+                }
+            }
+        });
     }
+
     // ---- epilogue ----
     // The tile's fp32 sums go through the ring's LDS (a lane: one row, four adjacent
     // columns) to threads of eight adjacent columns, so that every global access of the
