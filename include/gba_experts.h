@@ -50,7 +50,7 @@ const char *gbx_version(void);
  * grouped_gemm_act_grad takes as z). All `dtype` (gba_dtype). K == 0 gives
  * act(bias_e). workspace: NULL, or device memory that lets calls with few
  * output tiles split K (deterministic; contents neither needed nor kept).
- * Sizes: T < 2^31, N <= 2^23, K <= 2^21, else GBA_ERR_SHAPE. */
+ * Sizes: T <= 2^29, N <= 2^23, K <= 2^21, else GBA_ERR_SHAPE. */
 int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, const void *bias,
                           void *C, void *preact, int64_t T, int64_t E, int64_t N, int64_t K,
                           int act, int dtype, int flags, void *workspace, size_t workspace_bytes);
@@ -85,8 +85,9 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
  * value is a 4-bit E2M1 code (sign, then 0 .5 1 1.5 2 3 4 6).
  *   codes:  [M][K/2] bytes, code 2i in the low half of byte i.
  *   scales: [ceil(K/128)][M][4] bytes: block b of row m is byte b%4 of entry
- *           [b/4][m]; the bytes of blocks past K are written as 0. One plane
- *           feeds one matrix instruction step of 128 values. */
+ *           [b/4][m]; the bytes of blocks past K are written as 0, and a product
+ *           needs them to be no NaN (255). One plane feeds one matrix
+ *           instruction step of 128 values. */
 
 /* Quantise X [M,K] (`dtype`): s = floor(log2(max |x|)) - 2 + 127 over the block,
  * at least 0; codes nearest to x / 2^(s-127), ties to the even code, magnitudes

@@ -83,7 +83,9 @@ int check_enums(int act, int dtype) {
     return GBA_OK;
 }
 
-constexpr int64_t kMaxRows = 0x7fffffffLL;
+// Rows of a grouped product: 64 experts whose offsets decrease can claim 32 T rows
+// between them, in tiles of 16, which stays a 32-bit count. Rows of a quantised matrix: a 32-bit index.
+constexpr int64_t kMaxRows = 1LL << 29, kMaxQuantRows = 0x7fffffffLL;
 // A row pitch inside a tile's 32-bit byte offsets: 256 K-contiguous rows, or 64 rows along K.
 constexpr int64_t kMaxDepth = 1LL << 21, kMaxWidth = 1LL << 23;
 
@@ -263,7 +265,7 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
 int mx4_quantize(const void *X, void *codes, void *scales, int64_t M, int64_t K, int dtype) {
     int s = check_enums(GBA_ACT_NONE, dtype);
     if (s) return s;
-    if (M < 0 || K < 0 || M > kMaxRows || K > kMaxWidth) return GBA_ERR_SHAPE;
+    if (M < 0 || K < 0 || M > kMaxQuantRows || K > kMaxWidth) return GBA_ERR_SHAPE;
     if (K % 32) return GBA_ERR_ALIGN;
     const Span spans[] = {{X, size3(M, K, 2), true, false, 16},
                           {codes, size3(M, K / 2, 1), true, true, 16},
@@ -281,7 +283,7 @@ int mx4_dequantize(const void *codes, const void *scales, void *X, int64_t M, in
                    int dtype) {
     int s = check_enums(GBA_ACT_NONE, dtype);
     if (s) return s;
-    if (M < 0 || K < 0 || M > kMaxRows || K > kMaxWidth) return GBA_ERR_SHAPE;
+    if (M < 0 || K < 0 || M > kMaxQuantRows || K > kMaxWidth) return GBA_ERR_SHAPE;
     if (K % 32) return GBA_ERR_ALIGN;
     const Span spans[] = {{X, size3(M, K, 2), true, true, 16},
                           {codes, size3(M, K / 2, 1), true, false, 16},

@@ -151,8 +151,7 @@ __device__ __forceinline__ Found locate_few(const Group &g, int bm, int lane, F 
         n = ceil_div(rows, bm);
     }
     const int upto = wave_scan(n, lane);
-    // (Up to 64 experts of up to 2^31 / 16 row tiles overflow only for offsets that decrease.)
-    const int total = min((int)min((unsigned)__builtin_amdgcn_readlane(upto, 63), 0x7fffffffu), g.row_bound);
+    const int total = min(__builtin_amdgcn_readlane(upto, 63), g.row_bound);
     const int t = tile_of(total);
     Found f = {0, 0, 0, 0, 0, total};
     const unsigned long long past = __ballot(upto > t);

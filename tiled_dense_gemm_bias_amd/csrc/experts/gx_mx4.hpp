@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256)
 mx4_quantize_kernel(const uint16_t *__restrict__ X, uint32_t *__restrict__ codes,
                     uint32_t *__restrict__ scales, int M, int K) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    const long long row = (long long)blockIdx.x * kQuantRows + wid * 4 + (lane >> 4);
+    const long long row = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kQuantRows + wid * 4 + (lane >> 4);
     if (row >= M) return;   // whole 16-lane groups, so no block loses a lane
     const int plane0 = blockIdx.y * kQuantPlanes, k0 = plane0 * 128 + (lane & 15) * 8;
     const uint16_t *const x = X + (size_t)row * K;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256)
 mx4_dequantize_kernel(const uint32_t *__restrict__ codes, const uint32_t *__restrict__ scales,
                       uint16_t *__restrict__ X, int M, int K) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    const long long row = (long long)blockIdx.x * kQuantRows + wid * 4 + (lane >> 4);
+    const long long row = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kQuantRows + wid * 4 + (lane >> 4);
     if (row >= M) return;
     const int plane0 = blockIdx.y * kQuantPlanes, k0 = plane0 * 128 + (lane & 15) * 8;
     uint32_t c[kQuantPlanes], w[kQuantPlanes];
@@ -125,9 +125,11 @@ mx4_dequantize_kernel(const uint32_t *__restrict__ codes, const uint32_t *__rest
     }
 }
 
-// Grid: 16-row groups along x, groups of planes along y (K <= 2^23: at most 2^14).
+// Grid: 16-row groups along x and, beyond 2^20 of them, z; groups of planes along
+// y (K <= 2^23: at most 2^14).
 inline dim3 mx4_grid(int M, int K) {
-    return dim3((unsigned)ceil_div(M, kQuantRows), (unsigned)ceil_div(ceil_div(K, 128), kQuantPlanes));
+    const int groups = ceil_div(M, kQuantRows), z = ceil_div(groups, 1 << 20);
+    return dim3((unsigned)ceil_div(groups, z), (unsigned)ceil_div(ceil_div(K, 128), kQuantPlanes), (unsigned)z);
 }
 
 }  // namespace gbx
