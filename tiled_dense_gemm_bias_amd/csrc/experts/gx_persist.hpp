@@ -87,7 +87,11 @@ grouped_persist_kernel(Group g) {
     __shared__ __attribute__((aligned(1024))) char bias_smem[BIASED ? 2 * NW * 1024 : 16];
     constexpr int STG_BYTES = 16 * 64 * 2;
     __shared__ __attribute__((aligned(1024))) char stage_smem[NW * 2 * STG_BYTES];
-    static_assert(4 * TILE_BYTES + 2 * S_BYTES + 2 * NW * 1024 + NW * 2 * STG_BYTES <= 160 * 1024, "LDS");
+    // Where the loads that warm the L2 drop what they read (4-bit: no LDS left for it).
+    constexpr bool WARM = !MX;
+    constexpr int WARM_BY = 3;
+    __shared__ __attribute__((aligned(256))) char warm_smem[WARM ? 256 : 16];
+    static_assert(4 * TILE_BYTES + 2 * S_BYTES + 2 * NW * 1024 + NW * 2 * STG_BYTES + (WARM ? 256 : 0) <= 160 * 1024, "LDS");
 
     const int wid_s = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int K = g.K, N = g.N;   // rows mode: the depth; TA: the tile's (nk below)
@@ -263,6 +267,46 @@ grouped_persist_kernel(Group g) {
             buffer_load_lds16_at<S_REGION>(d.rs, (uint32_t)lane_now() * 16u, ld_wave + st);
         }
     };
+    // One load a wave and slice warms the L2 for the slice WARM_BY after the one whose loads
+    // have just gone out, one lane a 128-byte line: waves 0 and 1 a quarter of B's slice,
+    // waves 2 and 3 a quarter of A's; the tiles next to this one, at work on the same
+    // XCD, take the other quarters. What it reads lands in LDS that nothing reads. A
+    // slice's own loads have half a slice to a whole one (0.6 to 1.2 us) to arrive, too
+    // little for HBM, where a round's rows and weights come from when each expert has
+    // its own: 16384 x 8192 x 4096 bf16 by 8 experts 793 -> 751 us (one expert, whose
+    // weights the caches hold, 715 -> 720), weight gradients 835 -> 786. By two slices instead
+    // of three the same within 1 %, of B alone nothing, every line by its own tile 2 % less gain.
+    const uint32_t warm_lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(GBA_LDS void *)warm_smem);
+    const bool warm_b = wid_s < 2;
+    uint32_t warm_off = 0;   // this lane's line, from the slice's corner
+    auto set_warm = [&](const Tile &t) __attribute__((always_inline)) {
+        const bool wide = warm_b ? !TB : TA;
+        const uint32_t pitch = (uint32_t)(warm_b ? (TB ? K : N) : (TA ? g.M : K)) * 2u;
+        const int quarter = ((warm_b ? t.m0 : t.n0) >> 8) & 3, l = lane_now(), w = wid_s & 1;
+        warm_off = l >= 32 ? kOobOffset
+                   : wide  ? (uint32_t)(quarter * 16 + w * 8 + (l >> 2)) * pitch + (uint32_t)(l & 3) * 128u
+                           : (uint32_t)(quarter * 64 + w * 32 + l) * pitch;
+        asm volatile("" : "+v"(warm_off));
+    };
+    // Position and range of the slice WARM_BY after the one at p (`there`: not past the tile's last whole one).
+    auto warm_at = [&](const DmaPos &p) __attribute__((always_inline)) {
+        const uint16_t *const a = TA ? p.pa + (size_t)(WARM_BY * BK) * g.M : p.pa + WARM_BY * BK;
+        const uint16_t *const b = TB ? p.pb + WARM_BY * BK : p.pb + (size_t)(WARM_BY * BK) * N;
+        return warm_b ? b : a;
+    };
+    auto warm_bytes = [&](const DmaPos &p, bool there) __attribute__((always_inline)) {
+        const uint32_t n = warm_b ? p.nb - (TB ? 2u * WARM_BY * BK : 0u) : p.na - (TA ? 0u : 2u * WARM_BY * BK);
+        return there ? n : 0u;
+    };
+    auto warm = [&](__amdgpu_buffer_rsrc_t rs) __attribute__((always_inline)) {
+        asm volatile(
+            "s_mov_b32 m0, %2\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dword %0, %1, 0 offen lds"
+            :
+            : "v"(warm_off), "s"(rs), "s"(warm_lds)
+            : "memory", "m0");
+    };
     const uint32_t bias_lds = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(GBA_LDS void *)bias_smem + (uint32_t)(wid_s * 1024));
     auto bias_dma = [&](const Tile &t, int p) {
@@ -411,7 +455,6 @@ grouped_persist_kernel(Group g) {
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    auto no_payload = [](auto) __attribute__((always_inline)) {};
 
     Tile cur_t;
     if (!tile_of(0, cur_t)) return;
@@ -432,8 +475,12 @@ grouped_persist_kernel(Group g) {
         pos = pos_full(cur_t, true, 1);
         const SliceDma d1 = make_dma(pos);
         static_for<LDS_LOADS>([&](auto i_c) { dma_one(ld_wave + (uint32_t)TILE_BYTES, d1, i_c); });
+        if constexpr (WARM) {
+            set_warm(cur_t);
+            warm(make_rsrc(warm_at(pos), warm_bytes(pos, 2 + WARM_BY < cur_t.nk)));
+        }
     }
-    wait_vmcnt<LDS_LOADS>();
+    wait_vmcnt<LDS_LOADS + (WARM ? 1 : 0)>();
     block_barrier();
     auto read_first = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -453,7 +500,10 @@ grouped_persist_kernel(Group g) {
         Tile nxt_t;
         const bool nxt_live = tile_of(r + 1, nxt_t);
         if (!nxt_live) nxt_t = cur_t;
-        if (r > 0) set_offsets(cur_t, 1);
+        if (r > 0) {
+            set_offsets(cur_t, 1);
+            if constexpr (WARM) set_warm(cur_t);
+        }
         const int nk = cur_t.nk;
 
         auto slice = [&](int kt, auto first_c) __attribute__((always_inline)) {
@@ -489,11 +539,29 @@ grouped_persist_kernel(Group g) {
                 }
             };
             step(0, 1, std::true_type{}, delta, std::false_type{}, 0u, SliceDma{}, first_c, prep);
-            wait_vmcnt_lgkm0<0>();
+            wait_vmcnt_lgkm0<WARM ? 1 : 0>();   // all but the newest: the load that warms
             block_barrier();
             if (__builtin_expect(bias_next, 0)) bias_dma(nxt_t, (r + 1) & 1);
             __builtin_amdgcn_sched_barrier(0);
-            step(1, 0, std::false_type{}, 0, std::true_type{}, lds_cur, dn, std::false_type{}, no_payload);
+            const uint16_t *warm_p = nullptr;
+            uint32_t warm_n = 0;
+            __amdgpu_buffer_rsrc_t warm_rs = dn.rb;
+            step(1, 0, std::false_type{}, 0, std::true_type{}, lds_cur, dn, std::false_type{}, [&](auto q_c) __attribute__((always_inline)) {
+                // In pieces, beside matrix instructions that have no other company.
+                constexpr int q = decltype(q_c)::value;
+                if constexpr (WARM && q == NMF - 11) {
+                    warm_p = warm_at(pos);
+                    asm volatile("" : "+s"(warm_p));
+                } else if constexpr (WARM && q == NMF - 9) {
+                    warm_n = warm_bytes(pos, kt + 3 + WARM_BY < nk);
+                    asm volatile("" : "+s"(warm_n));
+                } else if constexpr (WARM && q == NMF - 6) {
+                    warm_rs = make_rsrc(warm_p, warm_n);
+                    asm volatile("" : "+s"(warm_rs));
+                } else if constexpr (WARM && q == NMF - 1) {
+                    warm(warm_rs);
+                }
+            });
             lds_cur += (uint32_t)delta;
             delta = -delta;
         };
