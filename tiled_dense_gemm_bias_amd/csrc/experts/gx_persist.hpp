@@ -630,7 +630,13 @@ grouped_persist_kernel(Group g) {
                 const __amdgpu_buffer_rsrc_t Cw = make_rsrc((uint16_t *)ga->C + corner, 0x7fffffffu);
                 const bool with_z = BIASED && !MX && ga->zout != nullptr;
                 const __amdgpu_buffer_rsrc_t Pw = make_rsrc(with_z ? ga->zout + corner : nullptr, with_z ? 0x7fffffffu : 0u);
-                f32x4 bq[4];
+                f32x4 bq[BIASED ? FN : 1];
+                if constexpr (BIASED) {
+#pragma unroll
+                    for (int f = 0; f < FN; ++f)
+                        bq[f] = has_bias ? *reinterpret_cast<const f32x4 *>(bias_mine + 512 + (16 * f + 4 * wg) * 4)
+                                         : f32x4{0.f, 0.f, 0.f, 0.f};
+                }
                 u32x2 zq[SLOPED ? 2 : 1][SLOPED ? ZB : 1][4];
                 // z of ZB groups (a lane: one row, four columns), a batch ahead of its use.
                 auto load_z = [&](int batch) __attribute__((always_inline)) {
@@ -639,7 +645,7 @@ grouped_persist_kernel(Group g) {
                     for (int b = 0; b < ZB; ++b)
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
-                            const int fh = (batch * ZB + b) / FM, fm = (batch * ZB + b) % FM;
+                            const int fh = (batch * ZB + b) & 1, fm = (batch * ZB + b) >> 1;
                             const uint32_t zo = z_off + (uint32_t)fm * 2u * pitch8 + (uint32_t)(fh * 128 + f * 32);
                             zq[batch & 1][b][f] = !masked || (fm * BD + wr < rows_left && fh * 64 + 16 * f + 4 * wg < cols_left)
                                                       ? *reinterpret_cast<const u32x2 *>(Zw + zo)
@@ -656,16 +662,8 @@ grouped_persist_kernel(Group g) {
                             v[j] = *reinterpret_cast<const u32x4 *>(sb + (8 * j + rr) * 128 + ((rc ^ (rr & 7)) * 16));
                     }
                     if (gi < NG) {
-                        const int fh = gi / FM, fm = gi % FM;
+                        const int fh = gi & 1, fm = gi >> 1;
                         char *const sb = stg + (gi & 1) * STG_BYTES;
-                        if (gi % FM == 0) {
-                            if constexpr (BIASED) {
-#pragma unroll
-                                for (int f = 0; f < 4; ++f)
-                                    bq[f] = has_bias ? *reinterpret_cast<const f32x4 *>(bias_mine + 512 + (16 * (4 * fh + f) + 4 * wg) * 4)
-                                                   : f32x4{0.f, 0.f, 0.f, 0.f};
-                            }
-                        }
                         if constexpr (SLOPED) {
                             if (gi == 0) load_z(0);
                             if (gi % ZB == 0 && gi + ZB < NG) load_z(gi / ZB + 1);
@@ -674,7 +672,7 @@ grouped_persist_kernel(Group g) {
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
                             s[f] = value(4 * fh + f, fm);
-                            if constexpr (BIASED) s[f] += bq[f];
+                            if constexpr (BIASED) s[f] += bq[4 * fh + f];
                         }
                         // This lane's 8 bytes of block f, in the staging buffer.
                         auto staged = [&](int f) __attribute__((always_inline)) {
@@ -714,7 +712,7 @@ grouped_persist_kernel(Group g) {
                         }
                     }
                     if (gi > 0) {
-                        const int fh = (gi - 1) / FM, fm = (gi - 1) % FM;
+                        const int fh = (gi - 1) & 1, fm = (gi - 1) >> 1;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             if (masked && (fm * BD + 8 * j + rr >= rows_left || fh * 64 + rc * 8 >= cols_left)) continue;
@@ -725,22 +723,55 @@ grouped_persist_kernel(Group g) {
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
-            // fp32 gradients: four adjacent values of one row a lane, 64 bytes a row and block.
-            auto store_f32 = [&](float *out) __attribute__((always_inline)) {
-                const bool add = (ga->flags & GF_ADD) != 0;
-                char *const Cw = reinterpret_cast<char *>(out + corner);
+            // fp32 gradients: the same way, 32 columns of 16 rows at a time, which fill the
+            // same staging buffers. Rows and columns past the edge get offsets out of range.
+            auto store_f32 = [&](float *out, auto add_c) __attribute__((always_inline)) {
+                constexpr bool ADD = decltype(add_c)::value;
+                // 64 rows of at most 2^25 bytes: offsets below 2^31.
+                const __amdgpu_buffer_rsrc_t Cw[2] = {make_rsrc(out + corner, 0x80000000u),
+                                                      make_rsrc(out + corner + (size_t)64 * N, 0x80000000u)};
+                const uint32_t at0 = (uint32_t)rr * (uint32_t)N * 4u + (uint32_t)rc * 16u;
+                constexpr int NF = FM * FN / 2;
+                u32x4 was[2][2];
 #pragma unroll
-                for (int fn = 0; fn < FN; ++fn) {
+                for (int gi = 0; gi <= NF; ++gi) {
+                    const int fm = gi / (FN / 2), fp = gi % (FN / 2);
+                    // Rows 8 j + rr, columns 4 rc .. 4 rc + 3 of group n.
+                    auto place = [&](int n, int j) __attribute__((always_inline)) {
+                        const int m = n / (FN / 2), p = n % (FN / 2);
+                        const bool ok = m * BD + 8 * j + rr < rows_left && p * 32 + 4 * rc < cols_left;
+                        return ok ? at0 + (uint32_t)(2 * (m % 4) + j) * 2u * pitch8 + (uint32_t)(p * 128) : kOobOffset;
+                    };
+                    u32x4 v[2];
+                    if (gi > 0) {
+                        const char *const sb = stg + ((gi - 1) & 1) * STG_BYTES;
 #pragma unroll
-                    for (int fm = 0; fm < FM; ++fm) {
-                        f32x4 a = value(fn, fm);
-                        if (fm * BD + wr < rows_left && fn * BD + 4 * wg < cols_left) {
-                            f32x4 *const p = reinterpret_cast<f32x4 *>(Cw + (2u * z_off + (uint32_t)fm * 4u * pitch8 + (uint32_t)(fn * 64)));
-                            if (add) a += *p;
-                            *p = a;
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
+                        for (int j = 0; j < 2; ++j)
+                            v[j] = *reinterpret_cast<const u32x4 *>(sb + (8 * j + rr) * 128 + ((rc ^ (rr & 7)) * 16));
                     }
+                    if (gi < NF) {
+                        char *const sb = stg + (gi & 1) * STG_BYTES;
+#pragma unroll
+                        for (int j = 0; ADD && j < 2; ++j)
+                            was[gi & 1][j] = __builtin_amdgcn_raw_buffer_load_b128(Cw[fm / 4], (int)place(gi, j), 0, 0);
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const f32x4 a = value(2 * fp + f, fm);
+                            *reinterpret_cast<f32x4 *>(sb + wr * 128 + (((4 * f + wg) ^ (wr & 7)) * 16)) = a;
+                        }
+                    }
+                    if (gi > 0) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            u32x4 o = v[j];
+                            if constexpr (ADD) {
+                                f32x4 a = __builtin_bit_cast(f32x4, v[j]) + __builtin_bit_cast(f32x4, was[(gi - 1) & 1][j]);
+                                o = __builtin_bit_cast(u32x4, a);
+                            }
+                            __builtin_amdgcn_raw_buffer_store_b128(o, Cw[(gi - 1) / (FN / 2) / 4], (int)place(gi - 1, j), 0, 0);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             };
             auto store_tile = [&](auto a_c) __attribute__((always_inline)) {
@@ -750,9 +781,12 @@ grouped_persist_kernel(Group g) {
                     store_all(std::true_type{}, a_c);
             };
             if constexpr (EPI == EPI_GRAD) {
-                if constexpr (ACT == GRAD_F32)
-                    store_f32((float *)ga->C);
-                else
+                if constexpr (ACT == GRAD_F32) {
+                    if (ga->flags & GF_ADD)
+                        store_f32((float *)ga->C, std::true_type{});
+                    else
+                        store_f32((float *)ga->C, std::false_type{});
+                } else
                     store_tile(std::integral_constant<int, ACT_NONE>{});
             } else if constexpr (EPI == EPI_SLOPE) {
                 store_tile(std::integral_constant<int, ACT_NONE>{});
