@@ -732,7 +732,8 @@ grouped_persist_kernel(Group g) {
                                                       make_rsrc(out + corner + (size_t)64 * N, 0x80000000u)};
                 const uint32_t at0 = (uint32_t)rr * (uint32_t)N * 4u + (uint32_t)rc * 16u;
                 constexpr int NF = FM * FN / 2;
-                u32x4 was[2][2];
+                constexpr int AHEAD = 4;   // groups whose old values are on their way
+                u32x4 was[AHEAD][2];
 #pragma unroll
                 for (int gi = 0; gi <= NF; ++gi) {
                     const int fm = gi / (FN / 2), fp = gi % (FN / 2);
@@ -742,6 +743,11 @@ grouped_persist_kernel(Group g) {
                         const bool ok = m * BD + 8 * j + rr < rows_left && p * 32 + 4 * rc < cols_left;
                         return ok ? at0 + (uint32_t)(2 * (m % 4) + j) * 2u * pitch8 + (uint32_t)(p * 128) : kOobOffset;
                     };
+                    auto load_was = [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            was[n % AHEAD][j] = __builtin_amdgcn_raw_buffer_load_b128(Cw[n / (FN / 2) / 4], (int)place(n, j), 0, 0);
+                    };
                     u32x4 v[2];
                     if (gi > 0) {
                         const char *const sb = stg + ((gi - 1) & 1) * STG_BYTES;
@@ -749,11 +755,12 @@ grouped_persist_kernel(Group g) {
                         for (int j = 0; j < 2; ++j)
                             v[j] = *reinterpret_cast<const u32x4 *>(sb + (8 * j + rr) * 128 + ((rc ^ (rr & 7)) * 16));
                     }
+                    if constexpr (ADD) {
+#pragma unroll
+                        for (int n = 0; gi == 0 && n < AHEAD - 1; ++n) load_was(n);
+                    }
                     if (gi < NF) {
                         char *const sb = stg + (gi & 1) * STG_BYTES;
-#pragma unroll
-                        for (int j = 0; ADD && j < 2; ++j)
-                            was[gi & 1][j] = __builtin_amdgcn_raw_buffer_load_b128(Cw[fm / 4], (int)place(gi, j), 0, 0);
 #pragma unroll
                         for (int f = 0; f < 2; ++f) {
                             const f32x4 a = value(2 * fp + f, fm);
@@ -765,12 +772,13 @@ grouped_persist_kernel(Group g) {
                         for (int j = 0; j < 2; ++j) {
                             u32x4 o = v[j];
                             if constexpr (ADD) {
-                                f32x4 a = __builtin_bit_cast(f32x4, v[j]) + __builtin_bit_cast(f32x4, was[(gi - 1) & 1][j]);
+                                f32x4 a = __builtin_bit_cast(f32x4, v[j]) + __builtin_bit_cast(f32x4, was[(gi - 1) % AHEAD][j]);
                                 o = __builtin_bit_cast(u32x4, a);
                             }
                             __builtin_amdgcn_raw_buffer_store_b128(o, Cw[(gi - 1) / (FN / 2) / 4], (int)place(gi - 1, j), 0, 0);
                         }
                     }
+                    if (ADD && gi + AHEAD - 1 < NF) load_was(gi + AHEAD - 1);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
