@@ -281,3 +281,19 @@ def test_many_short_rows_in_4_bits():
         want_codes, want_scales = orc.mx4_pack(c, s)
         assert torch.equal(codes[lo:lo + 100], want_codes) and torch.equal(scales[:, lo:lo + 100], want_scales)
         assert torch.equal(y[lo:lo + 100].double(), orc.mx4_values(c, s))
+
+
+def test_the_example_learns_and_serves():
+    """The layer of examples/expert_layer.py: its loss falls, its outputs in 4 bits stay near the 16-bit ones."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    say("example")
+    losses, error = ex.run(tokens=1000, experts=6, top=2, width=256, hidden=320, steps=12)
+    assert losses[-1] < 0.9 * losses[0], losses
+    # A code is off by up to a quarter of its value (5 of 4 .. 6), its root mean square about a
+    # tenth; four roundings (inputs, weights, twice) add up to some 0.2.
+    assert 0 < error < 0.4, error
