@@ -249,8 +249,12 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
         if ((s = current_cus(&cus))) return s;
         const gbx::Plan p = gbx::plan_grad(T, E, g.M, g.N, workspace ? workspace_bytes : 0, cus);
         const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_GRAD, 0, true>, gbx::launch_reduce<gbx::EPI_GRAD, 1, true>};
-        s = p.big ? hip_result(gbx::big_wgrad_tn[dtype][f32](g, t_stream))
-                  : launch_split(g, p, gbx::wgrad_tn[dtype][p.tile], gbx::part_tn[dtype][p.tile], reduce[dtype], workspace);
+        if (p.big) {   // with the bias gradient
+            g.sums = dbias;
+            const int kind = (f32 ? gbx::GRAD_F32 : gbx::GRAD_16) + (!dbias ? 0 : nk ? gbx::GRAD_SUMS_A : gbx::GRAD_SUMS_B);
+            return hip_result(gbx::big_wgrad_tn[dtype][kind](g, t_stream));
+        }
+        s = launch_split(g, p, gbx::wgrad_tn[dtype][p.tile], gbx::part_tn[dtype][p.tile], reduce[dtype], workspace);
         if (s) return s;
     }
     if (dbias) {

@@ -35,6 +35,7 @@ struct Group {
     const uint16_t *z;           // EPI_SLOPE: [T][N]
     void *C;
     uint16_t *zout;              // EPI_ACT: [T][N] or null
+    void *sums;                  // EPI_GRAD: [E][columns of dC] or null
     float *part;                 // EPI_PART: [splits][rows of C][N]
     int T, E, M, N, K;
     int act, flags, splits;

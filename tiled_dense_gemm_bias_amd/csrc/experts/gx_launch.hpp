@@ -34,7 +34,7 @@ extern const LaunchFn big_fwd_nn_f16[kNumActs], big_fwd_nn_bf16[kNumActs];
 extern const LaunchFn big_slope_nt_f16[kNumActs], big_slope_nt_bf16[kNumActs];
 extern const LaunchFn big_slope_nn_f16[kNumActs], big_slope_nn_bf16[kNumActs];
 extern const LaunchFn big_mx4_f16[kNumActs], big_mx4_bf16[kNumActs];   // by the output's type
-extern const LaunchFn big_wgrad_tn[2][2];   // [operand type][GRAD_16, GRAD_F32]
+extern const LaunchFn big_wgrad_tn[2][kNumGrads];   // [operand type][GRAD_*]
 
 }  // namespace gbx
 
@@ -62,17 +62,20 @@ extern const LaunchFn big_wgrad_tn[2][2];   // [operand type][GRAD_16, GRAD_F32]
     GBX_BIG_KERNEL_(OP, DT, gbx::EPI, 0, TB, false) GBX_BIG_KERNEL_(OP, DT, gbx::EPI, 1, TB, false) \
     GBX_BIG_KERNEL_(OP, DT, gbx::EPI, 2, TB, false) GBX_BIG_KERNEL_(OP, DT, gbx::EPI, 3, TB, false) \
     GBX_BIG_KERNEL_(OP, DT, gbx::EPI, 4, TB, false) GBX_BIG_KERNEL_(OP, DT, gbx::EPI, 5, TB, false)
-#define GBX_BIG_WGRAD_TABLE(NAME)                                                               \
-    GBX_BIG_KERNEL_(0, 0, gbx::EPI_GRAD, 0, false, true) GBX_BIG_KERNEL_(0, 0, gbx::EPI_GRAD, 1, false, true) \
-    GBX_BIG_KERNEL_(1, 1, gbx::EPI_GRAD, 0, false, true) GBX_BIG_KERNEL_(1, 1, gbx::EPI_GRAD, 1, false, true)
+#define GBX_BIG_WGRAD_(T)                                                                       \
+    GBX_BIG_KERNEL_(T, T, gbx::EPI_GRAD, 0, false, true) GBX_BIG_KERNEL_(T, T, gbx::EPI_GRAD, 1, false, true) \
+    GBX_BIG_KERNEL_(T, T, gbx::EPI_GRAD, 2, false, true) GBX_BIG_KERNEL_(T, T, gbx::EPI_GRAD, 3, false, true) \
+    GBX_BIG_KERNEL_(T, T, gbx::EPI_GRAD, 4, false, true) GBX_BIG_KERNEL_(T, T, gbx::EPI_GRAD, 5, false, true)
+#define GBX_BIG_WGRAD_TABLE(NAME) GBX_BIG_WGRAD_(0) GBX_BIG_WGRAD_(1)
 #else
 #define GBX_BIG_TABLE(NAME, OP, DT, EPI, TB)                                                    \
     const gbx::LaunchFn gbx::NAME[gba::kNumActs] = {                                            \
         gbx::launch_persist<OP, DT, gbx::EPI, 0, TB, false>, gbx::launch_persist<OP, DT, gbx::EPI, 1, TB, false>, \
         gbx::launch_persist<OP, DT, gbx::EPI, 2, TB, false>, gbx::launch_persist<OP, DT, gbx::EPI, 3, TB, false>, \
         gbx::launch_persist<OP, DT, gbx::EPI, 4, TB, false>, gbx::launch_persist<OP, DT, gbx::EPI, 5, TB, false>};
-#define GBX_BIG_WGRAD_TABLE(NAME)                                                               \
-    const gbx::LaunchFn gbx::NAME[2][2] = {                                                     \
-        {gbx::launch_persist<0, 0, gbx::EPI_GRAD, 0, false, true>, gbx::launch_persist<0, 0, gbx::EPI_GRAD, 1, false, true>}, \
-        {gbx::launch_persist<1, 1, gbx::EPI_GRAD, 0, false, true>, gbx::launch_persist<1, 1, gbx::EPI_GRAD, 1, false, true>}};
+#define GBX_BIG_WGRAD_(T)                                                                       \
+    {gbx::launch_persist<T, T, gbx::EPI_GRAD, 0, false, true>, gbx::launch_persist<T, T, gbx::EPI_GRAD, 1, false, true>, \
+     gbx::launch_persist<T, T, gbx::EPI_GRAD, 2, false, true>, gbx::launch_persist<T, T, gbx::EPI_GRAD, 3, false, true>, \
+     gbx::launch_persist<T, T, gbx::EPI_GRAD, 4, false, true>, gbx::launch_persist<T, T, gbx::EPI_GRAD, 5, false, true>}
+#define GBX_BIG_WGRAD_TABLE(NAME) const gbx::LaunchFn gbx::NAME[2][gbx::kNumGrads] = {GBX_BIG_WGRAD_(0), GBX_BIG_WGRAD_(1)};
 #endif

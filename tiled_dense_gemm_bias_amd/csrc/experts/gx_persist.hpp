@@ -62,8 +62,18 @@ __device__ __forceinline__ void mfma_gap() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// The ACT of an EPI_GRAD kernel names its output: 16 bits or fp32.
-enum { GRAD_16 = 0, GRAD_F32 = 1 };
+// acc += A.B as mfma_tied, with the sums in vector registers (bias gradients).
+template <int OP>
+__device__ __forceinline__ void mfma_ones(f32x4 &acc, const u32x4 &a, const u32x4 &b) {
+    if constexpr (OP == OP_F16)
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(acc) : "v"(a), "v"(b));
+    else
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(a), "v"(b));
+}
+
+// The ACT of an EPI_GRAD kernel names its output, 16 bits or fp32, and whether it
+// also sums the columns of dC (the bias gradient), its first factor or its second.
+enum { GRAD_16 = 0, GRAD_F32 = 1, GRAD_SUMS_A = 2, GRAD_SUMS_B = 4, kNumGrads = 6 };
 
 template <int OP, int ODT, int EPI, int ACT, bool TB, bool TA>
 __global__ void __launch_bounds__(256)
@@ -81,6 +91,8 @@ grouped_persist_kernel(Group g) {
     static_assert(!TA || (!TB && !MX), "layouts: nt, nn, tn");
     static_assert(!MX || TB, "4-bit operands are K-contiguous");
     constexpr bool BIASED = EPI == EPI_ACT;
+    constexpr bool GRAD = EPI == EPI_GRAD, SUMS_A = GRAD && (ACT & GRAD_SUMS_A) != 0;
+    constexpr bool SUMS = SUMS_A || (GRAD && (ACT & GRAD_SUMS_B) != 0);
 
     __shared__ __attribute__((aligned(1024))) char smem[4 * TILE_BYTES + 2 * S_BYTES];
     // A tile's bias, one 1 KiB slot per wave and per tile parity (see gemm_v5.hpp).
@@ -364,6 +376,24 @@ grouped_persist_kernel(Group g) {
     i16x4 fbl[2][FN], fbh[2][FN];
     u32x4 fw[2][FN];
     uint32_t sca[2][FM], scb[2][FN];
+    // The column sums of dC, as products with ones: one more matrix instruction for each of
+    // dC's fragments, in the tiles of the other factor's first 256 columns and the
+    // waves of its first 128. A pass of its own over dC took 54 us beside 744 (16384 rows,
+    // 8 experts of 8192 x 4096), these 21; kernels of their own, as the branch alone costs 20.
+    f32x4 sums[SUMS ? FM : 1];
+    constexpr uint32_t kOne = OP == OP_F16 ? 0x3c003c00u : 0x3f803f80u;
+    u32x4 ones = {kOne, kOne, kOne, kOne};
+    if constexpr (SUMS) asm volatile("" : "+v"(ones));
+    auto add_sums = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            if constexpr (SUMS_A)
+                mfma_ones<OP>(sums[f], ones, __builtin_bit_cast(u32x4, __builtin_shufflevector(fal[buf][f], fah[buf][f], 0, 1, 2, 3, 4, 5, 6, 7)));
+            else
+                mfma_ones<OP>(sums[f], __builtin_bit_cast(u32x4, __builtin_shufflevector(fbl[buf][f], fbh[buf][f], 0, 1, 2, 3, 4, 5, 6, 7)), ones);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
     auto read_one = [&](int buf, int kk, int r) __attribute__((always_inline)) {
         if (r < NFA) {
             if constexpr (TA) {
@@ -505,6 +535,15 @@ grouped_persist_kernel(Group g) {
             if constexpr (WARM) set_warm(cur_t);
         }
         const int nk = cur_t.nk;
+        // The wave that sums: of the tile in the other factor's first columns, the first of two.
+        const bool with_sums = SUMS && (SUMS_A ? cur_t.n0 == 0 && wid_s % WN == 0 : cur_t.m0 == 0 && wid_s / WN == 0);
+        if constexpr (SUMS) {
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                sums[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+                asm volatile("" : "+v"(sums[f]));
+            }
+        }
 
         auto slice = [&](int kt, auto first_c) __attribute__((always_inline)) {
             const bool here = kt + 2 < nk;
@@ -539,6 +578,8 @@ grouped_persist_kernel(Group g) {
                 }
             };
             step(0, 1, std::true_type{}, delta, std::false_type{}, 0u, SliceDma{}, first_c, prep);
+            if constexpr (SUMS)
+                if (with_sums) add_sums(0);
             wait_vmcnt_lgkm0<WARM ? 1 : 0>();   // all but the newest: the load that warms
             block_barrier();
             if (__builtin_expect(bias_next, 0)) bias_dma(nxt_t, (r + 1) & 1);
@@ -562,6 +603,8 @@ grouped_persist_kernel(Group g) {
                     warm(warm_rs);
                 }
             });
+            if constexpr (SUMS)
+                if (with_sums) add_sums(1);
             lds_cur += (uint32_t)delta;
             delta = -delta;
         };
@@ -788,8 +831,31 @@ grouped_persist_kernel(Group g) {
                 else
                     store_all(std::true_type{}, a_c);
             };
-            if constexpr (EPI == EPI_GRAD) {
-                if constexpr (ACT == GRAD_F32) {
+            if constexpr (GRAD) {
+                if constexpr (SUMS) {
+                    if (with_sums) {
+                        // SUMS_A: lane l has the sum of row l % 16 of block f (four times); else
+                        // lanes 0, 16, 32, 48 have four columns of block f each.
+                        const int width = SUMS_A ? ga->M : N;
+                        const int first = SUMS_A ? cur_t.m0 + wm_s * WTM + wr : cur_t.n0 + wn_s * WTN + 4 * wg;
+                        const bool add = (ga->flags & GF_ADD) != 0;
+#pragma unroll
+                        for (int f = 0; f < FM; ++f)
+#pragma unroll
+                            for (int i = 0; i < (SUMS_A ? 1 : 4); ++i) {
+                                const int at = first + f * BD + i;
+                                if ((SUMS_A ? wg : wr) != 0 || at >= width) continue;
+                                const size_t o = (size_t)cur_t.e * width + at;
+                                if constexpr ((ACT & GRAD_F32) != 0) {
+                                    float *const p = (float *)ga->sums + o;
+                                    *p = add ? *p + sums[f][i] : sums[f][i];
+                                } else {
+                                    ((uint16_t *)ga->sums)[o] = (uint16_t)pack2<ODT>(sums[f][i], 0.f);
+                                }
+                            }
+                    }
+                }
+                if constexpr ((ACT & GRAD_F32) != 0) {
                     if (ga->flags & GF_ADD)
                         store_f32((float *)ga->C, std::true_type{});
                     else
