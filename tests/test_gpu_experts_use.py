@@ -297,3 +297,34 @@ def test_the_example_learns_and_serves():
     # A code is off by up to a quarter of its value (5 of 4 .. 6), its root mean square about a
     # tenth; four roundings (inputs, weights, twice) add up to some 0.2.
     assert 0 < error < 0.4, error
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_large_products_of_more_experts_than_lanes(dtype):
+    """70 experts, empty ones among them, at sizes that the persistent kernels take: all three products."""
+    E, N, K, dt = 70, 2056, 1032, DT[dtype]
+    sizes = [(37 * e * e + 300) % 700 if e % 9 else 0 for e in range(E)]
+    say("70 experts", dtype, sum(sizes))
+    g = torch.Generator(device="cuda").manual_seed(31)
+    off, T = make_offsets(sizes, 3), sum(sizes) + 8
+    a, dc = draw(g, (T, K), dt), draw(g, (T, N), dt)
+    w, bias = draw(g, (E, N, K), dt, K ** -0.5), draw(g, (E, N), dt)
+    c, da = torch.full((T, N), float("nan"), dtype=dt, device="cuda"), torch.full((T, K), float("nan"), dtype=dt, device="cuda")
+    gba.grouped_gemm_bias_act(a, off, w, bias, c, "sigmoid", transpose_b=True)
+    z, err, owned = orc.product(a, off.tolist(), w, bias, True)
+    want = orc.act("sigmoid", z)
+    orc.check("c", c, want, orc.with_rounding(want, 0.25 * err + orc.ACT_TOL, dt), owned)
+    gba.grouped_gemm_act_grad(dc, off, w, a, da, "softplus", transpose_b=True)
+    d, err, _ = orc.product(dc, off.tolist(), w, None, False)
+    s = orc.slope("softplus", a.double())
+    orc.check("da", da, d * s, orc.with_rounding(d * s, s * err + orc.SLOPE_TOL * (d.abs() + err), dt), owned)
+    for tb in (True, False):
+        dw = torch.empty((E, N, K) if tb else (E, K, N), dtype=dt, device="cuda")
+        db = torch.empty(E, N, dtype=dt, device="cuda")
+        gba.grouped_gemm_wgrad(a, dc, off, dw, db, transpose_b=tb)
+        for e, b, n in orc.groups(off.tolist(), T):
+            x, y = a[b:b + n].double(), dc[b:b + n].double()
+            p = y.T.contiguous()
+            want, size = p @ x, p.abs() @ x.abs()
+            orc.check("dw", dw[e] if tb else dw[e].T, want, orc.with_rounding(want, size * orc.sum_rel(n), dt))
+            orc.check("db", db[e], y.sum(0), orc.with_rounding(y.sum(0), y.abs().sum(0) * orc.sum_rel(n), dt))

@@ -247,7 +247,7 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
         g.C = dW;
         int cus;
         if ((s = current_cus(&cus))) return s;
-        const gbx::Plan p = gbx::plan_grad(T, E, g.M, g.N, workspace ? workspace_bytes : 0, cus);
+        const gbx::Plan p = gbx::plan_grad(T, E, g.M, g.N, dbias != nullptr, workspace ? workspace_bytes : 0, cus);
         const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_GRAD, 0, true>, gbx::launch_reduce<gbx::EPI_GRAD, 1, true>};
         if (p.big) {   // with the bias gradient
             g.sums = dbias;

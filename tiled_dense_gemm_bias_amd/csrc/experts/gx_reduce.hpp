@@ -1,4 +1,5 @@
-// Second pass of a split sum: adds the splits' fp32 partial sums in split order
+// Second pass of a split sum, bound by its launch where splits pay (16 x 2816 of four
+// splits: 4.4 us): adds the splits' fp32 partial sums in split order
 // (the result does not depend on which was written first), then the epilogue.
 #pragma once
 
