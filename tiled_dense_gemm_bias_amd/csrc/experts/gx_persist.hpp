@@ -23,8 +23,8 @@
 // 2.1 GHz). 16384 rows by 8 even experts of 8192 x 4096 bf16: 728 us, 1.51 PFLOP/s, 74 % of
 // the cycles in matrix instructions; with uneven experts 770 (68 row tiles for 64),
 // with bias and GELU 842 (8 us of vector arithmetic a tile), with the pre-activations
-// 868. 8192 x 14336 x 4096 in 4 bits: 216 us, 252 with bias and GELU: a tile has 16
-// slices, and its epilogue and stores take as long as they.
+// 868. 8192 x 14336 x 4096 in 4 bits: 216 us, 4.45 PFLOP/s, 252 with bias and GELU: 16
+// slices a tile, of 1.5 us (1.7 GHz), then 7 us of stores and 5 of bias and GELU.
 #pragma once
 
 #include "gx_common.hpp"
