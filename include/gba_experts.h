@@ -9,6 +9,8 @@
  *     row-major. The library allocates nothing and keeps no pointer after a call.
  *   - Pointers must be 16-byte aligned (offsets: 4-byte); row lengths must be
  *     multiples of 8 values in 16 bits, of 32 values in 4 bits: GBA_ERR_ALIGN.
+ *   - A product has at most 2^29 rows (T; M of the dense 4-bit product), an
+ *     operand to be quantised less than 2^31: GBA_ERR_SHAPE.
  *   - Accumulation is fp32; each output is rounded once, to nearest even.
  *   - Argument errors are reported synchronously, before any launch. Work is
  *     enqueued on the calling thread's stream (gbx_set_stream) and runs
@@ -50,7 +52,7 @@ const char *gbx_version(void);
  * grouped_gemm_act_grad takes as z). All `dtype` (gba_dtype). K == 0 gives
  * act(bias_e). workspace: NULL, or device memory that lets calls with few
  * output tiles split K (deterministic; contents neither needed nor kept).
- * Sizes: T <= 2^29, N <= 2^23, K <= 2^21, else GBA_ERR_SHAPE. */
+ * Sizes: N <= 2^23, K <= 2^21, else GBA_ERR_SHAPE. */
 int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, const void *bias,
                           void *C, void *preact, int64_t T, int64_t E, int64_t N, int64_t K,
                           int act, int dtype, int flags, void *workspace, size_t workspace_bytes);

@@ -154,6 +154,14 @@ def test_mx4_refusals(lib):
     assert d(X=at(3)) == ALIAS
 
 
+@pytest.mark.parametrize("call", [fwd, grad, wgrad, mx4, dense4])
+def test_most_rows(lib, call):
+    """2^29 rows pass the size check (the next one, an output over an input, answers); one more does not."""
+    rows, out = ("M", "C") if call is dense4 else ("T", {fwd: "C", grad: "dA", wgrad: "dW", mx4: "C"}[call])
+    assert call(lib, **{rows: 1 << 29, out: at(1)}) == ALIAS
+    assert call(lib, **{rows: (1 << 29) + 1, out: at(1)}) == SHAPE
+
+
 def test_no_device_gives_device_error(lib):
     if _gpu_present():
         pytest.skip("a GPU is present; this checks the GPU-less path")
