@@ -168,11 +168,13 @@ __device__ __forceinline__ Found locate_few(const Group &g, int bm, int lane, F 
 // act'(z) in fp32. relu'(0) = 0; at z = +-inf the limit; NaN for NaN.
 //  sigmoid:   t / (1 + t)^2 with t = e^-|z| (no cancellation on either side).
 //  softplus:  the logistic of z.
-//  gelu:      Phi(z) + z phi(z) = q for z <= 0 and 1 - q for z > 0, with q =
-//             e^(-z^2/2) P(|z|): P, of degree 7, is fitted to (m(x) - x) / sqrt(2 pi)
-//             with m the Mills ratio Phi(-x) / phi(x)
-//             (tiled_dense_gemm_bias_amd/gelu_slope_fit.py), q within 4.1e-6. |z| is
-//             clamped in P only: at z = +-inf q is 0 and NaN stays NaN.
+//  gelu:      Phi(z) + z phi(z) = q for z <= 0 and 1 - q for z > 0, with x = |z|,
+//             q = e^(-x^2/2) (R(t) - x / sqrt(2 pi)), t = 1 / (1 + x/4): R, of degree 7,
+//             is fitted to m(x) / sqrt(2 pi), m the Mills ratio Phi(-x) / phi(x), for q's
+//             relative error (tiled_dense_gemm_bias_amd/gelu_slope_fit.py): within 2e-7,
+//             and for z < -1 within (1 + z^2/8) 3e-7 of itself (the rounding of the
+//             exponential's argument; z^2 is exact, as z has 16 bits). x is clamped
+//             outside the exponential only: at z = +-inf q is 0 and NaN stays NaN.
 //  gelu_tanh: z = tanh form; with s = 1 / (1 + e), e = e^(-2y),
 //             y = sqrt(2/pi) (z + c z^3): s + z s (1 - s) 2 y', and 1 - s = e s.
 //             Outside |z| = 10 the slope is 0 or 1 to 1e-30: z is clamped there,
@@ -189,15 +191,20 @@ __device__ __forceinline__ float act_slope(float z) {
     } else if constexpr (ACT == ACT_SOFTPLUS) {
         return act_fn<ACT_SIGMOID>(z);
     } else if constexpr (ACT == ACT_GELU) {
-        const float a = fminf(fabsf(z), 8.0f);
-        float p = fmaf(a, -0.00016855745343491435f, 0.002319070976227522f);
-        p = fmaf(a, p, -0.013923607766628265f);
-        p = fmaf(a, p, 0.049940045922994614f);
-        p = fmaf(a, p, -0.12582695484161377f);
-        p = fmaf(a, p, 0.2479596585035324f);
-        p = fmaf(a, p, -0.7976623773574829f);
-        p = fmaf(a, p, 0.49999603629112244f);
-        const float q = p * __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+        const float a = fminf(fabsf(z), 16.0f);
+        const float t = __builtin_amdgcn_rcpf(fmaf(a, 0.25f, 1.0f));
+        // R and x / sqrt(2 pi) by 1/8, the exponential by 8: the hardware's exponential is 0
+        // below 2^-126, and q, which is up to 5 times that there, would be lost sooner.
+        constexpr float s = 0.125f;
+        float r = fmaf(t, s * -0.0971691083497504f, s * 0.3682747148994894f);
+        r = fmaf(t, r, s * -0.3203441591740204f);
+        r = fmaf(t, r, s * 0.3387267891725851f);
+        r = fmaf(t, r, s * -0.0111699049002808f);
+        r = fmaf(t, r, s * 0.1251299008583134f);
+        r = fmaf(t, r, s * 0.0963644464504781f);
+        r = fmaf(t, r, s * 0.0001873002465777f);
+        const float p = fmaf(a, s * -0.3989422804014327f, r);
+        const float q = p * __builtin_amdgcn_exp2f(fmaf(z * z, -0.5f * kLog2e, 3.0f));
         return z > 0.0f ? 1.0f - q : q;
     } else if constexpr (ACT == ACT_GELU_TANH) {
         const float c = fminf(fmaxf(z, -10.0f), 10.0f);
