@@ -20,6 +20,7 @@
  *     asynchronously. Nothing synchronises, allocates or copies, so every entry
  *     point can be recorded in a HIP graph.
  *   - No output may overlap an input or another output: GBA_ERR_ALIAS.
+ *   - Unknown flag bits: GBA_ERR_SHAPE.
  *   - A launch failure returns GBA_ERR_HIP (gbx_last_hip_error() gives the
  *     code); a device that is not gfx950 GBA_ERR_DEVICE.
  *
@@ -64,7 +65,8 @@ int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, 
  * carried through the activation that made that input (A = act(z)).
  * dC: [T,N]; W and flags as in the forward call ([E,K,N], or [E,N,K] with
  * GBA_TRANSPOSE_B); z, dA: [T,K]. act GBA_ACT_NONE: dA = dC.W_e^T and z may be
- * NULL. relu'(0) is 0; at z = +-inf every derivative is its limit; NaN gives NaN. */
+ * NULL. relu'(0) is 0; at z = +-inf every derivative is its limit; NaN gives NaN.
+ * Sizes: N <= 2^21 (the depth of this product), K <= 2^23, else GBA_ERR_SHAPE. */
 int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W, const void *z,
                           void *dA, int64_t T, int64_t E, int64_t N, int64_t K, int act, int dtype,
                           int flags, void *workspace, size_t workspace_bytes);
