@@ -121,6 +121,28 @@ int grouped_gemm_bias_act_mx4(const void *a_codes, const void *a_scales, const i
                               int64_t T, int64_t E, int64_t N, int64_t K, int act, int dtype,
                               void *workspace, size_t workspace_bytes);
 
+/* What a call of these sizes runs on a device of `cus` compute units: the output
+ * tile of a workgroup, whether the persistent kernel walks such tiles, the K
+ * ranges whose partial sums a second pass joins (1: none), and whether the
+ * weights are read non-temporally. workspace_bytes: of a workspace that the call is given (0:
+ * none). T is M for the dense 4-bit product. Launches nothing and needs no device. Sizes as
+ * in the call: GBA_ERR_SHAPE, GBA_ERR_ALIGN; also GBA_ERR_SHAPE for another op, sizes of 0 or cus < 1. */
+enum {
+    GBX_FORWARD = 0,    /* grouped_gemm_bias_act */
+    GBX_ACT_GRAD = 1,   /* grouped_gemm_act_grad */
+    GBX_WGRAD = 2,      /* grouped_gemm_wgrad */
+    GBX_WGRAD_BIAS = 3, /* the same with dbias */
+    GBX_MX4 = 4         /* gemm_bias_act_mx4 (E = 1), grouped_gemm_bias_act_mx4 */
+};
+typedef struct {
+    int32_t tile_m, tile_n;
+    int32_t persistent;
+    int32_t splits;
+    int32_t non_temporal;
+} gbx_plan;
+int gbx_get_plan(int op, int64_t T, int64_t E, int64_t N, int64_t K, size_t workspace_bytes,
+                 int cus, gbx_plan *plan);
+
 #ifdef __cplusplus
 }
 #endif

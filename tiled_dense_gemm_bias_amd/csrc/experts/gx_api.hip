@@ -97,6 +97,16 @@ int check_sizes(int64_t T, int64_t E, int64_t depth, int64_t width) {
 
 size_t size3(int64_t a, int64_t b, int64_t c) { return (size_t)a * (size_t)b * (size_t)c; }
 
+// The choice of kernel of every product, from the arguments of its call.
+gbx::Plan plan_of(int op, int64_t T, int64_t E, int64_t N, int64_t K, size_t workspace, int cus) {
+    switch (op) {
+    case GBX_FORWARD: return gbx::plan_rows(T, E, N, K, workspace, cus);
+    case GBX_ACT_GRAD: return gbx::plan_rows(T, E, K, N, workspace, cus);
+    case GBX_MX4: return gbx::plan_rows(T, E, N, K / 4, workspace, cus);
+    default: return gbx::plan_grad(T, E, K, N, op == GBX_WGRAD_BIAS, workspace, cus);
+    }
+}
+
 // The ring kernel of a plan, then (a split) the second pass.
 int launch_split(gbx::Group &g, const gbx::Plan &p, const gbx::LaunchFn &whole, const gbx::LaunchFn &part,
                  const gbx::LaunchFn &reduce, void *workspace) {
@@ -155,7 +165,7 @@ int grouped_gemm_bias_act(const void *A, const int32_t *offsets, const void *W, 
     const bool nt = (flags & GBA_TRANSPOSE_B) != 0;
     int cus;
     if ((s = current_cus(&cus))) return s;
-    const gbx::Plan p = gbx::plan_rows(T, E, N, K, workspace ? workspace_bytes : 0, cus);
+    const gbx::Plan p = plan_of(GBX_FORWARD, T, E, N, K, workspace ? workspace_bytes : 0, cus);
     if (p.big) {
         const gbx::LaunchFn *const big[2][2] = {{gbx::big_fwd_nn_f16, gbx::big_fwd_nn_bf16},
                                                 {gbx::big_fwd_nt_f16, gbx::big_fwd_nt_bf16}};
@@ -199,7 +209,7 @@ int grouped_gemm_act_grad(const void *dC, const int32_t *offsets, const void *W,
     const bool nt = !(flags & GBA_TRANSPOSE_B);
     int cus;
     if ((s = current_cus(&cus))) return s;
-    const gbx::Plan p = gbx::plan_rows(T, E, K, N, workspace ? workspace_bytes : 0, cus);
+    const gbx::Plan p = plan_of(GBX_ACT_GRAD, T, E, N, K, workspace ? workspace_bytes : 0, cus);
     if (p.big) {
         const gbx::LaunchFn *const big[2][2] = {{gbx::big_slope_nn_f16, gbx::big_slope_nn_bf16},
                                                 {gbx::big_slope_nt_f16, gbx::big_slope_nt_bf16}};
@@ -247,7 +257,7 @@ int grouped_gemm_wgrad(const void *A, const void *dC, const int32_t *offsets, vo
         g.C = dW;
         int cus;
         if ((s = current_cus(&cus))) return s;
-        const gbx::Plan p = gbx::plan_grad(T, E, g.M, g.N, dbias != nullptr, workspace ? workspace_bytes : 0, cus);
+        const gbx::Plan p = plan_of(dbias ? GBX_WGRAD_BIAS : GBX_WGRAD, T, E, N, K, workspace ? workspace_bytes : 0, cus);
         const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_GRAD, 0, true>, gbx::launch_reduce<gbx::EPI_GRAD, 1, true>};
         if (p.big) {   // with the bias gradient
             g.sums = dbias;
@@ -339,7 +349,7 @@ static int mx4_common(const void *a_codes, const void *a_scales, const int32_t *
     g.splits = 1;
     int cus;
     if ((s = current_cus(&cus))) return s;
-    const gbx::Plan p = gbx::plan_rows(T, E, N, K / 4, workspace ? workspace_bytes : 0, cus);
+    const gbx::Plan p = plan_of(GBX_MX4, T, E, N, K, workspace ? workspace_bytes : 0, cus);
     if (p.big)
         return hip_result((dtype == GBA_DTYPE_F16 ? gbx::big_mx4_f16 : gbx::big_mx4_bf16)[act](g, t_stream));
     const gbx::LaunchFn reduce[2] = {gbx::launch_reduce<gbx::EPI_ACT, 0, false>, gbx::launch_reduce<gbx::EPI_ACT, 1, false>};
@@ -351,6 +361,22 @@ int gemm_bias_act_mx4(const void *a_codes, const void *a_scales, const void *w_c
                       int64_t K, int act, int dtype, void *workspace, size_t workspace_bytes) {
     return mx4_common(a_codes, a_scales, nullptr, false, w_codes, w_scales, bias, C, M, 1, N, K, act, dtype,
                       workspace, workspace_bytes);
+}
+
+int gbx_get_plan(int op, int64_t T, int64_t E, int64_t N, int64_t K, size_t workspace_bytes,
+                 int cus, gbx_plan *plan) {
+    if (!plan) return GBA_ERR_NULL;
+    if (op < GBX_FORWARD || op > GBX_MX4 || cus < 1 || T < 1 || N < 1 || K < 1) return GBA_ERR_SHAPE;
+    const bool grad = op == GBX_WGRAD || op == GBX_WGRAD_BIAS;
+    const int64_t depth = grad ? 0 : op == GBX_ACT_GRAD ? N : op == GBX_MX4 ? (K + 3) / 4 : K;
+    int s = check_sizes(T, E, depth, op == GBX_ACT_GRAD ? K : N);
+    if (!s && grad) s = check_sizes(T, E, 0, K);
+    if (s) return s;
+    if ((K % (op == GBX_MX4 ? 32 : 8)) || (N % 8)) return GBA_ERR_ALIGN;
+    const gbx::Plan p = plan_of(op, T, E, N, K, workspace_bytes, cus);
+    const gbx::TileCost &t = p.big ? gbx::kBig : grad ? gbx::kGradTileCost[p.tile] : gbx::kRowTiles[p.tile];
+    *plan = {t.bm, t.bn, p.big, p.splits, p.stream};
+    return GBA_OK;
 }
 
 int grouped_gemm_bias_act_mx4(const void *a_codes, const void *a_scales, const int32_t *offsets,

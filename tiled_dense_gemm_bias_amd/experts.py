@@ -32,6 +32,10 @@ ACCUMULATE = 32
 _LIB = None
 
 
+class _Plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile_m", "tile_n", "persistent", "splits", "non_temporal")]
+
+
 def _lib():
     global _LIB
     if _LIB is None:
@@ -47,6 +51,7 @@ def _lib():
             "mx4_dequantize": [p, p, p, i64, i64, ci],
             "gemm_bias_act_mx4": [p] * 6 + [i64] * 3 + [ci, ci, p, sz],
             "grouped_gemm_bias_act_mx4": [p] * 7 + [i64] * 4 + [ci, ci, p, sz],
+            "gbx_get_plan": [ci] + [i64] * 4 + [sz, ci, ctypes.POINTER(_Plan)],
             "gbx_set_stream": [p],
             "gbx_last_hip_error": [],
             "gbx_version": [],
@@ -67,6 +72,20 @@ def experts_lib():
 
 def experts_version() -> str:
     return _lib().gbx_version().decode()
+
+
+_OPS = {"forward": 0, "act_grad": 1, "wgrad": 2, "wgrad_bias": 3, "mx4": 4}
+
+
+def plan(op, T, E, N, K, workspace=0, cus=256) -> dict:
+    """What a call of these sizes runs on a device of `cus` compute units, given a workspace of
+    that many bytes: tile_m, tile_n, persistent, splits, non_temporal. op: "forward", "act_grad", "wgrad",
+    "wgrad_bias" (with dbias) or "mx4" (dense: E = 1). Needs no device."""
+    p = _Plan()
+    st = _lib().gbx_get_plan(_OPS[op], T, E, N, K, workspace, cus, ctypes.byref(p))
+    if st != 0:
+        raise GbaError(st, "gbx_get_plan")
+    return {n: getattr(p, n) for n, _ in _Plan._fields_}
 
 
 # The calls below run in a few microseconds of host time, as long as the smallest
