@@ -74,17 +74,24 @@ inline Plan plan_rows(int64_t T, int64_t E, int64_t cols, int64_t words, size_t 
     }
     // The persistent kernel's stream needs two slices.
     if (slices >= 2 && big_cost(row_tiles(T, E, 256) * ceil(cols / 256.0), slices, cus) < least) best = {true, 0, 1, false};
-    // B read once (about one row tile an expert), and too large for the 256 MiB
-    // cache behind the L2 to hold until the next call: read non-temporally (12 of
-    // 32 experts of 2816 x 2048 bf16, 16 rows: 36 -> 32 us; a B that the cache
-    // holds is 10 to 25 % slower so). Few tiles are then split in four, so that more of
-    // them read at once (32 -> 28 us; 2048 tiles: 60 us whole, 71 split; 22 slices: 28 and 36).
-    const double some = E < T ? E : T, b_bytes = 2.0 * E * cols * words;
+    // B read once (about one row tile an expert), and what one call reads of it, at most min(E, T)
+    // experts, too large for the 256 MiB cache behind the L2 to hold until the next
+    // call: read non-temporally (12 of 32 experts of 2816 x 2048 bf16, 16 rows: 36 -> 32 us; a B that
+    // the cache holds is 10 to 25 % slower so). Up to five such tiles a CU are then split in four where that
+    // gains more than the second pass takes. Two things are lost whole: the CUs' last round of
+    // tiles is half empty on average, 0.08 us a slice; and rows of a multiple of 4 KiB lie in
+    // few memory channels, which four places along K spread out, 0.08 us a slice and tile a CU up to
+    // two. Measured for 1 to 4 rows on 8 experts, over 0.5 to 5 tiles a CU, split against whole: rows of
+    // 30 slices +9 % (-5 to +26), 40 +3 % (-8 to +19); of 32 slices, 4 KiB, -4 % (-14 to +7), 64 -9 %
+    // (-22 to -2). 12 of 32 experts of 2816 x 2048: 34 -> 28 us.
+    const double some = E < T ? E : T, b_bytes = 2.0 * some * cols * words;
     const TileCost &t = kRowTiles[best.tile];
     if (!best.big && t.bm <= 64 && T / some <= t.bm && b_bytes > 128.0 * 1024 * 1024) {
         best.stream = true;
-        const double tiles = row_tiles(T, E, t.bm) * ceil((double)cols / t.bn);
-        if (t.bm <= 32 && best.splits == 1 && tiles <= 5.0 * cus && slices >= 32 && 16.0 * T * cols <= (double)workspace)
+        const double n = row_tiles(T, E, t.bm) * ceil((double)cols / t.bn) / cus;
+        const double lost = slices * (0.08 + (words % 2048 == 0 ? 0.08 * fmin(n, 2) : 0));
+        if (t.bm <= 32 && best.splits == 1 && n <= 5 && lost > reduce_cost((double)T * cols, 4) &&
+            16.0 * T * cols <= (double)workspace)
             best.splits = 4;
     }
     return best;
