@@ -1,10 +1,10 @@
-// What the kernels of libgba_experts share: the arguments of a grouped product,
-// the search for the expert and tile of a work unit, activation slopes, and the
-// microscaled 4-bit matrix instruction.
+// What the kernels of libgba_experts share: the groups (gx_groups.hpp), activation slopes,
+// the epilogue of eight outputs, and the microscaled 4-bit matrix instruction.
 #pragma once
 
 #include "gba_dma.hpp"
 #include "gemm_v3.hpp"   // mfma16x16x32, aswz, bswz
+#include "gx_groups.hpp"
 
 namespace gbx {
 
@@ -24,40 +24,7 @@ enum {
     EPI_PART = 3    // fp32 partial sums of one split
 };
 
-// A grouped product. Rows mode (weight gradients: see wgrad below): the rows of expert e of A [T][K] times
-// B_e, giving rows of C [T][N]. wgrad: At_e^T.B_e over the rows of expert e, with
-// At [T][M] and B [T][N], giving C [E][M][N]. K counts 16-bit words.
-struct Group {
-    const uint16_t *A, *B;
-    const uint32_t *sa, *sb;     // MX4 scale planes of A and B, one dword a row
-    const int32_t *offsets;      // null: one expert, all T rows
-    const uint16_t *bias;        // [E][N] or null
-    const uint16_t *z;           // EPI_SLOPE: [T][N]
-    void *C;
-    uint16_t *zout;              // EPI_ACT: [T][N] or null
-    void *sums;                  // EPI_GRAD: [E][columns of dC] or null
-    float *part;                 // EPI_PART: [splits][rows of C][N]
-    int T, E, M, N, K;
-    int act, flags, splits;
-    int row_bound;               // rows mode: most row tiles the grid was made for
-};
-// EPI_GRAD: fp32 output, added to what is there; B read once and too large to stay in the caches.
-enum { GF_F32 = 1, GF_ADD = 2, GF_STREAM = 4 };
-
-__device__ __forceinline__ int clamp_row(int v, int T) { return min(max(v, 0), T); }
-
-// First row and row count of expert e: offsets clamped to [0, T].
-__device__ __forceinline__ void expert_rows(const Group &g, int e, int &start, int &rows) {
-    if (!g.offsets) {
-        start = 0;
-        rows = g.T;
-        return;
-    }
-    start = clamp_row(g.offsets[e], g.T);
-    rows = max(clamp_row(g.offsets[e + 1], g.T) - start, 0);
-}
-
-// The same for a uniform e, into scalar registers by scalar loads (no kernel
+// expert_rows for a uniform e, into scalar registers by scalar loads (no kernel
 // writes the offsets), which wait for no vector memory.
 __device__ __forceinline__ void expert_rows_uniform(const Group &g, int e, int &start, int &rows) {
     int lo = 0, hi = g.T;
@@ -67,100 +34,9 @@ __device__ __forceinline__ void expert_rows_uniform(const Group &g, int e, int &
         lo = o[e];
         hi = o[e + 1];
     }
-    start = __builtin_amdgcn_readfirstlane(clamp_row(lo, g.T));
-    rows = __builtin_amdgcn_readfirstlane(max(clamp_row(hi, g.T) - start, 0));
-}
-
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-
-// Row tiles of all experts (rows mode), each wave for itself: lane l takes
-// experts l, l + 64, ... Offsets that decrease can name more tiles than the
-// grid was made for; those are left out.
-__device__ __forceinline__ int total_row_tiles(const Group &g, int bm, int lane) {
-    long long n = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-        int t = 0;
-        if (e0 + lane < g.E) {
-            int start, rows;
-            expert_rows(g, e0 + lane, start, rows);
-            t = ceil_div(rows, bm);
-        }
-        n += t;
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) n += __shfl_xor(n, d);
-    return __builtin_amdgcn_readfirstlane((int)min(n, (long long)g.row_bound));
-}
-
-// Most row tiles that T rows of E experts can make: one for each full tile, and
-// one more for each expert that has rows.
-inline long long row_tile_bound(long long T, long long E, int bm) {
-    return T / bm + (E < T ? E : T);
-}
-
-// The expert that row tile number t (in expert order) lies in, with the number of
-// row tiles before it, its tiles, rows and first row; `total` is that of total_row_tiles, and the
-// rest is set where t < total. Every lane gets the same answer.
-struct Found {
-    int e, before, tiles, start, rows, total;
-};
-__device__ __forceinline__ Found found_at(int e0, unsigned long long past, int before, int upto, int n, int start, int rows) {
-    const int l = __builtin_amdgcn_readfirstlane(__ffsll(past) - 1);
-    Found f;
-    f.e = e0 + l;
-    f.tiles = __builtin_amdgcn_readlane(n, l);
-    f.before = before + __builtin_amdgcn_readlane(upto, l) - f.tiles;
-    f.start = __builtin_amdgcn_readlane(start, l);
-    f.rows = __builtin_amdgcn_readlane(rows, l);
-    return f;
-}
-__device__ __forceinline__ Found find_row_tile(const Group &g, int bm, int t, int lane) {
-    Found f = {0, 0, 0, 0, 0, 0};
-    int before = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-        int n = 0, start = 0, rows = 0;
-        if (e0 + lane < g.E) {
-            expert_rows(g, e0 + lane, start, rows);
-            n = ceil_div(rows, bm);
-        }
-        const int upto = wave_scan(n, lane);
-        const unsigned long long past = __ballot(before + upto > t);
-        if (past) {
-            f = found_at(e0, past, before, upto, n, start, rows);
-            break;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
-    }
-    return f;
-}
-
-// For up to 64 experts, one reading of the offsets for both the total and the
-// tile: `tile_of(total)` gives the row tile wanted, or -1.
-template <class F>
-__device__ __forceinline__ Found locate_few(const Group &g, int bm, int lane, F &&tile_of) {
-    int n = 0, start = 0, rows = 0;
-    if (lane < g.E) {
-        expert_rows(g, lane, start, rows);
-        n = ceil_div(rows, bm);
-    }
-    const int upto = wave_scan(n, lane);
-    const int total = min(__builtin_amdgcn_readlane(upto, 63), g.row_bound);
-    const int t = tile_of(total);
-    Found f = {0, 0, 0, 0, 0, total};
-    const unsigned long long past = __ballot(upto > t);
-    if (t >= 0 && past) {
-        f = found_at(0, past, 0, upto, n, start, rows);
-        f.total = total;
-    }
-    return f;
+    rows_between(lo, hi, g.T, start, rows);
+    start = __builtin_amdgcn_readfirstlane(start);
+    rows = __builtin_amdgcn_readfirstlane(rows);
 }
 
 // ------------------------------------------------------- activation slopes --

@@ -158,23 +158,11 @@ grouped_persist_kernel(Group g) {
             t.nk = max(ceil_div(t.klen, BK), 2);
         } else {
             const int rt = idx / tiles_n;
-            int before, tiles;
-            if (few) {
-                const unsigned long long past = __ballot(upto > rt);
-                t.e = __builtin_amdgcn_readfirstlane(__ffsll(past) - 1);
-                before = t.e > 0 ? __builtin_amdgcn_readlane(upto, t.e - 1) : 0;
-                tiles = __builtin_amdgcn_readlane(upto, t.e) - before;
-                t.start = __builtin_amdgcn_readlane(start_l, t.e);
-                t.rows = __builtin_amdgcn_readlane(rows_l, t.e);
-            } else {
-                const Found f = find_row_tile(g, BM, rt, lane_now());
-                t.e = f.e;
-                before = f.before;
-                tiles = f.tiles;
-                t.start = f.start;
-                t.rows = f.rows;
-            }
-            grouped_tile(idx - before * tiles_n, tiles, tiles_n, 4, tm, tn);
+            const Found f = few ? few_row_tile(upto, start_l, rows_l, rt) : find_row_tile(g, BM, rt, lane_now());
+            t.e = f.e;
+            t.start = f.start;
+            t.rows = f.rows;
+            grouped_tile(idx - f.before * tiles_n, f.tiles, tiles_n, 4, tm, tn);
             t.klen = K;
             t.nk = ceil_div(K, BK);
         }
