@@ -98,7 +98,10 @@ inline Plan plan_rows(int64_t T, int64_t E, int64_t cols, int64_t words, size_t 
 }
 
 // Weight gradients: E products of M x N, summed over T / E rows on average. With
-// the bias gradient (`sums`) the ring kernel costs another launch, the persistent one does not.
+// the bias gradient (`sums`) the ring kernel costs another launch, the persistent one does
+// not. (The column sums of few long experts take longer than a launch, one of 16384 rows 29 us;
+// the persistent kernel has few tiles there and is no choice: with the measured time in place of 4 us
+// no plan of one to four experts from 2048 rows on changes.)
 inline Plan plan_grad(int64_t T, int64_t E, int64_t M, int64_t N, bool sums, size_t workspace, int cus) {
     const double slices = ceil((double)T / E / 64.0);
     Plan best = {false, GRAD_64x64, 1, false};
