@@ -62,7 +62,7 @@ struct Span {
 bool overlap(const Span &a, const Span &b) {
     if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
     const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x < y + b.bytes && y < x + a.bytes;
+    return x < y ? y - x < a.bytes : x - y < b.bytes;   // sums of address and size could wrap round
 }
 
 template <int N>
