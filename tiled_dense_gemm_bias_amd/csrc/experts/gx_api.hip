@@ -368,7 +368,7 @@ int gbx_get_plan(int op, int64_t T, int64_t E, int64_t N, int64_t K, size_t work
     if (!plan) return GBA_ERR_NULL;
     if (op < GBX_FORWARD || op > GBX_MX4 || cus < 1 || T < 1 || N < 1 || K < 1) return GBA_ERR_SHAPE;
     const bool grad = op == GBX_WGRAD || op == GBX_WGRAD_BIAS;
-    const int64_t depth = grad ? 0 : op == GBX_ACT_GRAD ? N : op == GBX_MX4 ? (K + 3) / 4 : K;
+    const int64_t depth = grad ? 0 : op == GBX_ACT_GRAD ? N : op == GBX_MX4 ? K / 4 : K;
     int s = check_sizes(T, E, depth, op == GBX_ACT_GRAD ? K : N);
     if (!s && grad) s = check_sizes(T, E, 0, K);
     if (s) return s;
