@@ -288,9 +288,8 @@ int mx4_quantize(const void *X, void *codes, void *scales, int64_t M, int64_t K,
     if (M == 0 || K == 0) return GBA_OK;
     if ((s = check_device())) return s;
     auto *const kernel = dtype == GBA_DTYPE_F16 ? gbx::mx4_quantize_kernel<0> : gbx::mx4_quantize_kernel<1>;
-    hipLaunchKernelGGL(kernel, gbx::mx4_grid((int)M, (int)K), dim3(256), 0, t_stream, (const uint16_t *)X,
-                       (uint32_t *)codes, (uint32_t *)scales, (int)M, (int)K);
-    return hip_result(hipGetLastError());
+    return hip_result(gbx::launch(kernel, gbx::mx4_grid((int)M, (int)K), dim3(256), t_stream, (const uint16_t *)X,
+                                  (uint32_t *)codes, (uint32_t *)scales, (int)M, (int)K));
 }
 
 int mx4_dequantize(const void *codes, const void *scales, void *X, int64_t M, int64_t K,
@@ -306,9 +305,8 @@ int mx4_dequantize(const void *codes, const void *scales, void *X, int64_t M, in
     if (M == 0 || K == 0) return GBA_OK;
     if ((s = check_device())) return s;
     auto *const kernel = dtype == GBA_DTYPE_F16 ? gbx::mx4_dequantize_kernel<0> : gbx::mx4_dequantize_kernel<1>;
-    hipLaunchKernelGGL(kernel, gbx::mx4_grid((int)M, (int)K), dim3(256), 0, t_stream, (const uint32_t *)codes,
-                       (const uint32_t *)scales, (uint16_t *)X, (int)M, (int)K);
-    return hip_result(hipGetLastError());
+    return hip_result(gbx::launch(kernel, gbx::mx4_grid((int)M, (int)K), dim3(256), t_stream, (const uint32_t *)codes,
+                                  (const uint32_t *)scales, (uint16_t *)X, (int)M, (int)K));
 }
 
 // offsets null: dense (E == 1).

@@ -57,9 +57,7 @@ column_sums_kernel(Group g) {
 
 template <int DT, int COLS, int NT>
 hipError_t launch_sums(const Group &g, hipStream_t stream) {
-    hipLaunchKernelGGL((column_sums_kernel<DT, COLS, NT>), dim3((unsigned)ceil_div(g.N, COLS), (unsigned)g.E), dim3(NT),
-                       0, stream, g);
-    return hipGetLastError();
+    return launch(column_sums_kernel<DT, COLS, NT>, dim3((unsigned)ceil_div(g.N, COLS), (unsigned)g.E), dim3(NT), stream, g);
 }
 
 // 64 columns are a 128-byte line of a row. Long experts take eight waves, so that

@@ -10,6 +10,18 @@ namespace gbx {
 
 using namespace gba;
 
+// Launches a kernel and returns that launch's status. (hipGetLastError after a launch would also
+// report what an earlier call of this thread left, and a split product stop half way.)
+template <class T>
+struct Exactly {
+    using type = T;
+};
+template <class... Args>
+hipError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, hipStream_t stream, typename Exactly<Args>::type... args) {
+    void *pointers[] = {&args...};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, block, pointers, 0, stream);
+}
+
 // Operand types. MX4 rows are counted in 16-bit words of four codes: a row of K
 // values is K / 4 words, and a 64-word slice (128 bytes) is 256 values, so the
 // 4-bit kernels move the same bytes in the same tiles as the 16-bit ones; only

@@ -888,9 +888,8 @@ hipError_t launch_persist(Group g, hipStream_t stream) {
     int cus = 0;
     const hipError_t e = current_cus(&cus);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((grouped_persist_kernel<OP, ODT, EPI, ACT, TB, TA>), dim3((unsigned)(tiles < cus ? tiles : cus)),
-                       dim3(256), 0, stream, g);
-    return hipGetLastError();
+    return launch(grouped_persist_kernel<OP, ODT, EPI, ACT, TB, TA>, dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(256),
+                  stream, g);
 }
 
 }  // namespace gbx

@@ -50,8 +50,7 @@ hipError_t launch_reduce(Group g, hipStream_t stream) {
     const long long rows = TA ? (long long)g.E * g.M : (long long)g.T, groups = (rows + 3) / 4;
     const long long z = groups < 32768 ? 1 : (groups + 32767) / 32768;   // grid dimensions of at most 2^16
     const dim3 grid((unsigned)ceil_div(g.N, 512), (unsigned)((groups + z - 1) / z), (unsigned)z);
-    hipLaunchKernelGGL((grouped_reduce_kernel<EPI, ODT, TA>), grid, dim3(256), 0, stream, g);
-    return hipGetLastError();
+    return launch(grouped_reduce_kernel<EPI, ODT, TA>, grid, dim3(256), stream, g);
 }
 
 }  // namespace gbx

@@ -401,9 +401,7 @@ hipError_t launch_ring(Group g, hipStream_t stream) {
     if (units <= 0) return hipSuccess;
     if (units > 0x7fffffffLL - kGridX) return hipErrorInvalidValue;
     g.row_bound = (int)row_tiles;
-    hipLaunchKernelGGL((grouped_ring_kernel<BM, BN, WM, WN, STAGES, OP, ODT, EPI, TB, TA>), tile_grid(units),
-                       dim3(256), 0, stream, g);
-    return hipGetLastError();
+    return launch(grouped_ring_kernel<BM, BN, WM, WN, STAGES, OP, ODT, EPI, TB, TA>, tile_grid(units), dim3(256), stream, g);
 }
 
 }  // namespace gbx
