@@ -16,8 +16,8 @@
 // What bounds it: with few rows an expert, HBM (each weight is read once: 16 rows on
 // 12 of 32 experts of 2816 x 2048 bf16 take 23 us, 6.0 TB/s; 5 x 14336 x 4096 in 4
 // bits 8.5 us, 3.7 TB/s, 16 slices being mostly latency); with tens of rows, loads and
-// matrix instructions about equally (999 rows on 15 experts, 1408 x 2048 fp16: 19 us,
-// 300 TFLOP/s). 128 x 128 is the largest tile of which two workgroups share a CU; larger
+// matrix instructions about equally (999 rows on 15 experts, 1408 x 2048 fp16: 19 to 23 us by
+// their shares, 250 to 300 TFLOP/s). 128 x 128 is the largest tile of which two workgroups share a CU; larger
 // products are the persistent kernel's.
 #pragma once
 

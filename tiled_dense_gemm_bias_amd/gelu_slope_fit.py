@@ -56,7 +56,8 @@ def slope(z, coeffs=COEFFS):
     for k in coeffs[-2::-1]:
         r = (d(r) * d(t) + d(f(k / 8))).astype(f)                          # fma
     p = (d(a) * d(f(-0.3989422804014327 / 8)) + d(r)).astype(f)
-    e = (d((z * z).astype(f)) * d(f(-0.7213475204444817)) + 3).astype(f)
+    with np.errstate(over="ignore"):                                       # z^2 past the largest fp32: e^-inf
+        e = (d((z * z).astype(f)) * d(f(-0.7213475204444817)) + 3).astype(f)
     q = (p * np.exp2(e).astype(f)).astype(f)
     return np.where(z > 0, f(1) - q, q)
 
