@@ -597,11 +597,20 @@ _EXPERTS = ("gemm_bias_act_mx4", "grouped_gemm_act_grad", "grouped_gemm_bias_act
             "mx4_quantize", "mx4_scales_shape", "mx4_unpack_scales")
 
 
+# Routing, movement of rows and 8-bit products by blocks: moe.py (libgba_moe.so), likewise.
+_MOE = ("fp8_dequantize", "fp8_dequantize_weights", "fp8_quantize", "fp8_quantize_weights",
+        "fp8_scales_shape", "fp8_weight_scales_shape", "gemm_act_grad_fp8_block",
+        "gemm_bias_act_fp8_block", "grouped_gemm_act_grad_fp8_block",
+        "grouped_gemm_bias_act_fp8_block", "moe_combine", "moe_combine_grad", "moe_dispatch",
+        "moe_route", "moe_route_grad", "moe_sort", "moe_sort_workspace")
+
+
 def __getattr__(name):
-    if name == "experts" or name in _EXPERTS:
-        import importlib
-        module = importlib.import_module(__name__ + ".experts")
-        for n in _EXPERTS:
-            globals()[n] = getattr(module, n)
-        return globals().get(name, module)
+    for part, names in (("experts", _EXPERTS), ("moe", _MOE)):
+        if name == part or name in names:
+            import importlib
+            module = importlib.import_module(__name__ + "." + part)
+            for n in names:
+                globals()[n] = getattr(module, n)
+            return globals().get(name, module)
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -25,8 +25,9 @@ hipError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, hipStream_t st
 // Operand types. MX4 rows are counted in 16-bit words of four codes: a row of K
 // values is K / 4 words, and a 64-word slice (128 bytes) is 256 values, so the
 // 4-bit kernels move the same bytes in the same tiles as the 16-bit ones; only
-// the matrix instruction and its scales differ.
-enum { OP_F16 = 0, OP_BF16 = 1, OP_MX4 = 2 };
+// the matrix instruction and its scales differ. F8 rows (8-bit floats with fp32 scales by blocks of 128)
+// are K / 2 words, a slice 128 values: one block, and one matrix instruction of 128.
+enum { OP_F16 = 0, OP_BF16 = 1, OP_MX4 = 2, OP_F8 = 3 };
 
 // What the kernel does with a tile's fp32 sums.
 enum {
@@ -187,6 +188,12 @@ __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa
     const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const i32x8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// A.B on 16 x 16 x 128 blocks of 8-bit codes (E4M3): lane l holds row / column l % 16 and 32 codes, the same
+// places of the 128 in both operands. Results lie as those of the 16-bit 16x16x32 instruction.
+__device__ __forceinline__ f32x4 mfma_f8(const i32x8 &a, const i32x8 &b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
 }  // namespace gbx

@@ -16,7 +16,8 @@ using namespace gba;
 // and B [T][N], giving C [E][M][N]. K counts 16-bit words.
 struct Group {
     const uint16_t *A, *B;
-    const uint32_t *sa, *sb;     // MX4 scale planes of A and B, one dword a row
+    const uint32_t *sa, *sb;     // MX4 scale planes of A and B, one dword a row; F8: fp32, planes of A, blocks
+                                 // of B [E][N / 128][K / 128] (rounded up)
     const int32_t *offsets;      // null: one expert, all T rows
     const uint16_t *bias;        // [E][N] or null
     const uint16_t *z;           // EPI_SLOPE: [T][N]

@@ -40,23 +40,24 @@ template <int BM, int BN, int WM, int WN, int STAGES, int OP, int ODT, int EPI, 
 __global__ void __launch_bounds__(256, 2)   // two workgroups a CU at least
 grouped_ring_kernel(Group g) {
     constexpr int NT = 256, BK = 64;
-    constexpr bool MX = OP == OP_MX4;
+    constexpr bool MX = OP == OP_MX4, F8 = OP == OP_F8;
     constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
     constexpr int CHT = BM / 8, CHB = BN / 8;   // chunks per k row of At's and B's tiles
     constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-    // MX4: a slice's scales, 2 planes of one dword a row for A, then for B
-    constexpr int S_BYTES = MX ? 8 * (BM + BN) : 0;
+    // MX4: a slice's scales, 2 planes of one dword a row for A, then for B. F8: A's plane.
+    constexpr int S_BYTES = MX ? 8 * (BM + BN) : F8 ? 4 * BM : 0;
     constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
     // Loads of a slice per thread. A tile of fewer than 256 chunks is loaded
     // by every group of waves that it fills, the same bytes to the same place.
     constexpr int A_LD = BM * 8 >= NT ? BM * 8 / NT : 1, B_LD = BN * 8 / NT;
     constexpr int AW = BM * 8 >= NT ? 4 : BM * 8 / 64;   // waves that a load of A fills
-    constexpr int LD = A_LD + B_LD + (MX ? 1 : 0);
+    constexpr int LD = A_LD + B_LD + (MX || F8 ? 1 : 0);
     static_assert(WM * WN == 4 && WTM % 16 == 0 && WTN % 16 == 0, "four waves of whole MFMA blocks");
     static_assert(BN * 8 % NT == 0 && (BM * 8 % NT == 0 || NT % (BM * 8) == 0), "loads split evenly");
     static_assert(!TA || (CHT >= 8 && !TB && !MX), "At: 64 rows or more");
     static_assert(TB || CHB >= 8, "B swizzle needs 8 chunks per row");
     static_assert(!MX || (TB && BM <= 256 && BN <= 256), "4-bit operands are K-contiguous");
+    static_assert(!F8 || (TB && !TA && BM >= 16 && BM <= 1024 && 128 % BN == 0), "8-bit operands: K-contiguous, one block of B's columns");
     static_assert(STAGES * STAGE <= 160 * 1024 && (STAGES - 1) * LD < 64, "ring");
 
     __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
@@ -164,7 +165,7 @@ grouped_ring_kernel(Group g) {
     struct {
         const uint16_t *pa, *pb;
         uint32_t na, nb;
-        const uint32_t *ps;   // MX4: this wave's scale plane: w % 2 of A's (w < 2) or B's
+        const uint32_t *ps;   // MX4: this wave's scale plane: w % 2 of A's (w < 2) or B's. F8: A's
         uint32_t ns;
         int left;             // slices left to load
     } pos;
@@ -190,6 +191,7 @@ grouped_ring_kernel(Group g) {
         }
         // 32 words: 128 values a plane
         if (MX && (pos.left <= 0 || (2 * (kt0 + kt) + (wid & 1)) * 32 >= K)) pos.ns = 0;
+        if (F8 && pos.left <= 0) pos.ns = 0;
     };
     {
         const int k0 = kt0 * BK;
@@ -213,6 +215,10 @@ grouped_ring_kernel(Group g) {
                      (size_t)(2 * kt0 + (wid & 1)) * plane_dwords;
             pos.ns = (uint32_t)(wid < 2 ? rows_a : rows_b) * 4u;
         }
+        if constexpr (F8) {
+            pos.ps = g.sa + (size_t)kt0 * g.T + start + m0;
+            pos.ns = (uint32_t)rows_a * 4u;
+        }
     }
     // Loads the next slice, which is slice kt of this unit, into stage S.
     auto load_slice = [&](int kt, auto stage_c) __attribute__((always_inline)) {
@@ -234,6 +240,12 @@ grouped_ring_kernel(Group g) {
                                  (wid < 2 ? (uint32_t)((wid & 1) * BM * 4) : (uint32_t)(2 * BM * 4 + (wid & 1) * BN * 4));
             if (lane * 4 < (wid < 2 ? BM : BN)) buffer_load_lds16(rs, (uint32_t)lane * 16u, dst);
             pos.ps += 2 * plane_dwords;
+        }
+        if constexpr (F8) {
+            // A quarter of the tile's rows a wave, one lane of it at least.
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(pos.ps, pos.ns);
+            if (lane * 16 < BM) buffer_load_lds16(rs, (uint32_t)(wid * BM + lane * 16), base + (uint32_t)(A_BYTES + B_BYTES + wid * BM));
+            pos.ps += g.T;
         }
         if constexpr (TA) {
             pos.pa += (size_t)BK * M;
@@ -307,8 +319,37 @@ grouped_ring_kernel(Group g) {
             for (int b = 0; b < FM; ++b) {
                 if constexpr (MX)
                     acc[a][b] = mfma_mx4(f.b[a], f.a[b], acc[a][b], f.sb[a], f.sa[b]);
-                else
+                else if constexpr (!F8)
                     acc[a][b] = mfma16x16x32<OP>(f.b[a], f.a[b], acc[a][b]);
+            }
+    };
+
+    // F8: one matrix instruction is one block of K. Its sums are scaled as they are added: by A's scale of the row
+    // (a lane's four sums share a row) times B's of the tile's columns, which comes by a scalar load a slice
+    // ahead. The 128 values lie across the lanes as chunks tg and 4 + tg, in both operands alike.
+    typedef const float __attribute__((address_space(4))) *ScalePtr;
+    ScalePtr wscales = nullptr;
+    float wscale = 0.f, wscale_next = 0.f;
+    if constexpr (F8) {
+        const int blocks = ceil_div(K, BK);
+        wscales = (ScalePtr)(uintptr_t)((const float *)g.sb + ((size_t)e * ceil_div(N, 128) + n0 / 128) * blocks + kt0);
+        if (nk > 0) wscale_next = wscales[0];
+    }
+    auto multiply_f8 = [&](const char *base, const Frags &f0, const Frags &f1) __attribute__((always_inline)) {
+        const auto both = [](const u32x4 &x, const u32x4 &y) __attribute__((always_inline)) {
+            return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+        };
+        float s[FM];
+#pragma unroll
+        for (int b = 0; b < FM; ++b)
+            s[b] = *reinterpret_cast<const float *>(base + A_BYTES + B_BYTES + (wm * WTM + b * 16 + tj) * 4) * wscale;
+#pragma unroll
+        for (int a = 0; a < FN; ++a)
+#pragma unroll
+            for (int b = 0; b < FM; ++b) {
+                const f32x4 p = mfma_f8(both(f0.b[a], f1.b[a]), both(f0.a[b], f1.a[b]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(p[i], s[b], acc[a][b][i]);
             }
     };
 
@@ -324,11 +365,22 @@ grouped_ring_kernel(Group g) {
                 wait_vmcnt_lgkm0<(STAGES - 2) * LD>();
                 block_barrier();
                 const char *const base = smem + S * STAGE;
+                if constexpr (F8) {
+                    wscale = wscale_next;
+                    wscale_next = wscales[min(kb + S + 1, nk - 1)];
+                }
                 constexpr std::integral_constant<int, (S + STAGES - 1) % STAGES> freed{};
                 // A ring of two stages has its next slice only now to ask for: first of
                 // all. Longer ones ask while their first fragments are on the way (small tiles
                 // 5 to 20 % faster so, 128 x 128 15 % slower).
-                if constexpr (STAGES == 2) {
+                if constexpr (F8) {
+                    Frags f0, f1;
+                    if constexpr (STAGES == 2) load_slice(kb + S + 1, freed);
+                    read_frags(base, 0, f0);
+                    read_frags(base, 1, f1);
+                    if constexpr (STAGES > 2) load_slice(kb + S + STAGES - 1, freed);
+                    multiply_f8(base, f0, f1);
+                } else if constexpr (STAGES == 2) {
                     load_slice(kb + S + 1, freed);
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {

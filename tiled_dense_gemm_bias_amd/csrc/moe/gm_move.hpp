@@ -1,0 +1,155 @@
+// Movement of rows between tokens and experts. rows[t][j] is the row of slot (t, j), or -1; a
+// number outside [0, R) counts as -1.
+//
+//   dispatch:      out[rows[t][j]] = x[t]
+//   combine:       out[t] = sum_j w[t][j] y[rows[t][j]], in 32 bits in the order of j
+//   combine_grad:  dy[rows[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[rows[t][j]]>
+//
+// HBM is what bounds them: every row is read and written once (a token's x and dout once for its k slots).
+// A workgroup takes one token and up to 8 KiB of its row: eight values a lane and load, a
+// token's loads all out before the first is used.
+#pragma once
+
+#include "gm_common.hpp"
+
+namespace gbm {
+
+struct Move {
+    const uint16_t *x, *y;     // tokens' rows [T][H]; experts' rows [R][H]
+    const int32_t *rows;       // [T][k]
+    const float *w;            // [T][k] or null (ones)
+    uint16_t *out, *dy;
+    float *dw;                 // [T][k] or null
+    int T, k, H, R;
+};
+
+constexpr int kMoveThreads = 256;
+
+__device__ __forceinline__ long long move_token() { return (long long)blockIdx.z * gridDim.y + blockIdx.y; }
+
+// Grid: pieces of a row along x, tokens along y and z.
+inline dim3 move_grid(long long tokens, int pieces) {
+    const long long z = (tokens + 32767) / 32768;
+    return dim3((unsigned)pieces, (unsigned)((tokens + z - 1) / z), (unsigned)z);
+}
+
+__global__ void __launch_bounds__(kMoveThreads)
+dispatch_kernel(Move a) {
+    const long long t = move_token();
+    const int h = (blockIdx.x * kMoveThreads + threadIdx.x) * 8;
+    if (t >= a.T || h >= a.H) return;
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.H + h);
+    const int32_t *const rows = a.rows + (size_t)t * a.k;
+    for (int j = 0; j < a.k; ++j) {
+        const int r = rows[j];
+        if ((unsigned)r < (unsigned)a.R) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(a.out + (size_t)r * a.H + h));
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack8(const u32x4 &x, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = to_f32<DT>(x[i] & 0xffffu);
+        v[2 * i + 1] = to_f32<DT>(x[i] >> 16);
+    }
+}
+template <int DT>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+    return u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMoveThreads)
+combine_kernel(Move a) {
+    const long long t = move_token();
+    const int h = (blockIdx.x * kMoveThreads + threadIdx.x) * 8;
+    if (t >= a.T || h >= a.H) return;
+    const int32_t *const rows = a.rows + (size_t)t * a.k;
+    float sum[8] = {};
+    constexpr int N = 8;
+    for (int j0 = 0; j0 < a.k; j0 += N) {
+        u32x4 v[N];
+        float w[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int r = j0 + j < a.k ? rows[j0 + j] : -1;
+            const bool there = (unsigned)r < (unsigned)a.R;
+            v[j] = u32x4{0u, 0u, 0u, 0u};
+            if (there) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.y + (size_t)r * a.H + h));
+            // A slot without a row adds w 0: a weight of NaN shows.
+            w[j] = j0 + j >= a.k ? 0.0f : a.w ? a.w[(size_t)t * a.k + j0 + j] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float f[8];
+            unpack8<DT>(v[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
+        }
+    }
+    __builtin_nontemporal_store(pack8<DT>(sum), reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.H + h));
+}
+
+// Columns that a thread of combine_grad holds of dout at a time.
+constexpr int kGradPieces = 4, kGradColumns = kMoveThreads * 8 * kGradPieces, kMaxSlots = 32;
+
+template <int DT>
+__global__ void __launch_bounds__(kMoveThreads)
+combine_grad_kernel(Move a) {
+    __shared__ float dots[kMoveThreads / 64][kMaxSlots];
+    const long long t = move_token();
+    if (t >= a.T) return;   // a whole workgroup
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const int32_t *const rows = a.rows + (size_t)t * a.k;
+    for (int j = lane; j < kMaxSlots; j += 64) dots[wid][j] = 0.0f;
+    wave_sync();
+    for (int h0 = 0; h0 < a.H; h0 += kGradColumns) {
+        float d[kGradPieces][8];
+#pragma unroll
+        for (int p = 0; p < kGradPieces; ++p) {
+            const int h = h0 + (p * kMoveThreads + threadIdx.x) * 8;
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (h < a.H) v = *reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.H + h);
+            unpack8<DT>(v, d[p]);
+        }
+        for (int j = 0; j < a.k; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r >= (unsigned)a.R) continue;
+            const float w = a.w ? a.w[(size_t)t * a.k + j] : 1.0f;
+            u32x4 v[kGradPieces];
+#pragma unroll
+            for (int p = 0; p < kGradPieces; ++p) {
+                const int h = h0 + (p * kMoveThreads + threadIdx.x) * 8;
+                v[p] = u32x4{0u, 0u, 0u, 0u};
+                if (h < a.H) v[p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.y + (size_t)r * a.H + h));
+            }
+            float dot = 0.0f;
+#pragma unroll
+            for (int p = 0; p < kGradPieces; ++p) {
+                const int h = h0 + (p * kMoveThreads + threadIdx.x) * 8;
+                float f[8], o[8];
+                unpack8<DT>(v[p], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot = fmaf(d[p][i], f[i], dot);
+                    o[i] = w * d[p][i];
+                }
+                if (a.dy && h < a.H) __builtin_nontemporal_store(pack8<DT>(o), reinterpret_cast<u32x4 *>(a.dy + (size_t)r * a.H + h));
+            }
+#pragma unroll
+            for (int s = 1; s < 64; s *= 2) dot += __shfl_xor(dot, s);
+            if (lane == 0) dots[wid][j] += dot;
+        }
+    }
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (a.dw && j < a.k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kMoveThreads / 64; ++w) s += dots[w][j];
+        a.dw[(size_t)t * a.k + j] = s;
+    }
+}
+
+}  // namespace gbm

@@ -1,0 +1,29 @@
+// Choice of tile and K split for an 8-bit product (host only).
+#pragma once
+
+#include "../experts/gx_plan.hpp"
+
+namespace gbm {
+
+using gbx::Plan;
+
+inline Plan plan_f8(int64_t T, int64_t E, int64_t cols, int64_t K, size_t workspace, int cus) {
+    const double slices = ceil(K / 128.0);
+    Plan best = {false, gbx::TILE_16x64, 1, false};
+    double least = 1e300;
+    for (int i = 0; i < gbx::kTiles; ++i) {
+        const gbx::TileCost &t = gbx::kRowTiles[i];
+        const double tiles = gbx::row_tiles(T, E, t.bm) * ceil((double)cols / t.bn);
+        for (int s : gbx::kSplits) {
+            if (s > 1 && (2 * s > slices || (double)s * T * cols * 4.0 > (double)workspace)) break;
+            const double c = gbx::ring_cost(t, tiles * s, ceil(slices / s), cus) + (s > 1 ? gbx::reduce_cost((double)T * cols, s) : 0);
+            if (c < least) {
+                least = c;
+                best = {false, i, s, false};
+            }
+        }
+    }
+    return best;
+}
+
+}  // namespace gbm

@@ -1,0 +1,554 @@
+// Routing to experts: each token's k best of E experts, their weights, and the sorting of the
+// (token, expert) slots by expert.
+//
+// Selection. A row belongs to G lanes (16, or 64 from 257 experts on), lane l holding experts
+// l, l + G, ... Each expert's value is a 64-bit float whose low 10 bits are replaced by
+// the expert's number, so that one maximum finds the best value and its expert, ties going to the
+// lowest number. Without a bias and without sums over groups the value is the logit itself (the
+// scores' order, exact in every type); otherwise it is score + bias in 64 bits, cut to 42: values
+// that differ by less count as ties. (In 32 bits about one in 10^5 rows of 256 experts chose
+// another expert than the formulas do.) A lane sorts its own values once, then k rounds take the
+// largest of the G first ones and move up the winner's list.
+//
+// Groups: the keys go through LDS, where lane g scans group g for its best one or two.
+//
+// The weights are computed from the chosen logits in 32 bits, renormalised sigmoid weights as
+// ratios that do not underflow together: s_i e^-min(m, 0), m the largest chosen logit.
+//
+// What bounds it: instructions. 16384 rows of 256 fp32 logits, k = 8, are 17 MB (3.3 us at 5.1 TB/s).
+#pragma once
+
+#include "gm_common.hpp"
+
+namespace gbm {
+
+constexpr int kMaxExperts = 1024, kMaxTop = 32, kMaxGroups = 16;
+constexpr int kRouteWaves = 8, kRouteThreads = kRouteWaves * 64;
+enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
+
+struct Route {
+    const void *x;         // [T][E]
+    const float *bias;     // [E] or null
+    int32_t *indices;      // [T][k]
+    float *weights;        // [T][k]
+    int32_t *counts;       // [blocks][E]: this block's slots of each expert (null: no sort follows)
+    int T, E, k;
+    int groups, top_groups, group_best, group_size;
+    int score, renorm, dtype;
+    float scale;
+    int tokens;            // per block
+};
+
+// One slot array sorted by expert: see sort_block.
+struct Sort {
+    const int32_t *indices;   // [T k]
+    const int32_t *counts;    // [blocks][E]
+    int32_t *offsets;         // [E + 1]
+    int32_t *rows;            // [T k]
+    int32_t *slots;           // [T k] or null
+    int n, E;                 // slots, experts
+    int per_block, blocks;    // slots a block
+};
+
+constexpr unsigned long long kExpertBits = 1023;
+
+// The value with the expert's number in its low bits: of two equal values the lower number's key is
+// the larger. v is finite.
+__device__ __forceinline__ double key_of(double v, int e) {
+    v += 0.0;   // -0 to +0
+    const unsigned long long b = __double_as_longlong(v), low = (unsigned long long)((long long)b < 0 ? e : 1023 - e);
+    return __longlong_as_double((long long)((b & ~kExpertBits) | low));
+}
+__device__ __forceinline__ int expert_of(double key) {
+    const long long b = __double_as_longlong(key);
+    const int low = (int)(b & (long long)kExpertBits);
+    return b < 0 ? low : 1023 - low;
+}
+__device__ __forceinline__ double without_expert(double key) {
+    return __longlong_as_double(__double_as_longlong(key) & ~(long long)kExpertBits);
+}
+
+// f over the 16 lanes of a row, or over the wave; every lane gets the result.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const long long b = __double_as_longlong(v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xf, 0xf, true);
+    const unsigned hi = (unsigned)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+__device__ __forceinline__ float lane_value(float v, int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); }
+__device__ __forceinline__ double lane_value(double v, int l) {
+    const long long b = __double_as_longlong(v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)b, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(b >> 32), l);
+    return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+template <int G, class T, class F>
+__device__ __forceinline__ T all_reduce(T v, F f) {
+    v = f(v, dpp<0x128>(v));   // row_ror 8, 4, 2, 1
+    v = f(v, dpp<0x124>(v));
+    v = f(v, dpp<0x122>(v));
+    v = f(v, dpp<0x121>(v));
+    if constexpr (G == 64) v = f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
+    return v;
+}
+struct Max {
+    __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+    __device__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
+};
+struct Sum {
+    template <class T>
+    __device__ T operator()(T a, T b) const { return a + b; }
+};
+// Whether any of a row's lanes says so. `first`: the row's first lane.
+template <int G>
+__device__ __forceinline__ bool any_of(bool b, int first) {
+    const unsigned long long m = __ballot(b);
+    return G == 64 ? m != 0 : ((m >> first) & 0xffff) != 0;
+}
+
+// Largest first (Batcher's odd-even merge sort).
+template <int P>
+__device__ __forceinline__ void sort_keys(double (&v)[P]) {
+#pragma unroll
+    for (int p = 1; p < P; p *= 2)
+#pragma unroll
+        for (int q = p; q > 0; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < P; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < P && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const double a = v[i + j], b = v[i + j + q];
+                        v[i + j] = __builtin_fmax(a, b);
+                        v[i + j + q] = __builtin_fmin(a, b);
+                    }
+}
+
+__device__ __forceinline__ float logit(const void *x, int dtype, size_t at) {
+    if (dtype == DTYPE_F32) return ((const float *)x)[at];
+    const uint32_t h = ((const uint16_t *)x)[at];
+    return dtype == DT_BF16 ? to_f32<DT_BF16>(h) : to_f32<DT_F16>(h);
+}
+
+// t_i of the chosen logits (t_i / sum t is the renormalised weight) and, for sigmoid scores,
+// s_i e^-min(m, 0) with m the largest: no common underflow.
+__device__ __forceinline__ float chosen_score(int score, float x, float m) {
+    if (score == SCORE_SOFTMAX) return expf(x - m);
+    return x >= 0 ? 1.0f / (1.0f + expf(-x)) : expf(x - fminf(m, 0.0f)) / (1.0f + expf(x));
+}
+
+template <int G, int P, bool GROUPED>
+__global__ void __launch_bounds__(kRouteThreads)
+route_kernel(Route a) {
+    constexpr int RPW = 64 / G;                        // rows a wave
+    constexpr int RPB = kRouteWaves * RPW;             // rows a block and pass
+    __shared__ double keys_smem[GROUPED ? RPB * G * P : 1];
+    __shared__ int count_smem[kMaxExperts];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const int l = lane & (G - 1), first = lane - l;
+    const double none = -__builtin_inf();
+    const long long t0 = (long long)linear_block() * a.tokens;
+    const int mine = (int)min((long long)a.tokens, a.T - t0);
+
+    if (a.counts) {
+        for (int e = tid; e < a.E; e += kRouteThreads) count_smem[e] = 0;
+        __syncthreads();
+    }
+    for (int pass = 0; pass < mine; pass += RPB) {
+        const int r = pass + wid * RPW + lane / G;
+        const bool live = r < mine;
+        const size_t row = (size_t)(t0 + (live ? r : 0)) * a.E;
+        float x[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = p * G + l;
+            x[p] = live && e < a.E ? logit(a.x, a.dtype, row + e) : -__builtin_inff();
+        }
+        // ---- values ----
+        const bool scored = a.bias != nullptr || (GROUPED && a.group_best > 1);
+        float m = -__builtin_inff();
+        bool bad = false;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            m = fmaxf(m, x[p]);
+            bad |= x[p] != x[p];
+        }
+        float z = 0.0f;      // softmax: the sum of e^(x - m)
+        double key[P];
+        if (a.score == SCORE_SOFTMAX) {
+            m = all_reduce<G>(m, Max{});
+            bad |= m == __builtin_inff();
+        }
+        if (scored) {
+            double total = 1.0;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                if (a.score == SCORE_SOFTMAX)
+                    key[p] = x[p] == -__builtin_inff() ? 0.0 : exp_to_one((double)x[p] - (double)m);
+                else
+                    key[p] = 1.0 / (1.0 + exp(-(double)x[p]));
+            }
+            if (a.score == SCORE_SOFTMAX) {
+                double sum = 0.0;
+#pragma unroll
+                for (int p = 0; p < P; ++p) sum += key[p];
+                sum = all_reduce<G>(sum, Sum{});
+                z = (float)sum;
+                total = sum > 0.0 ? 1.0 / sum : 0.0;
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int e = p * G + l;
+                float b = 0.0f;
+                if (a.bias && e < a.E) b = a.bias[e];
+                bad |= b != b;
+                if (b == -__builtin_inff()) x[p] = b;   // never chosen
+                key[p] = key[p] * total + (double)b;
+            }
+        } else {
+            if (a.score == SCORE_SOFTMAX && !a.renorm) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int p = 0; p < P; ++p) sum += x[p] == -__builtin_inff() ? 0.0f : expf(x[p] - m);
+                z = all_reduce<G>(sum, Sum{});
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) key[p] = (double)x[p];
+        }
+        bad = any_of<G>(bad, first);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            key[p] = bad || x[p] == -__builtin_inff() ? none : key_of(__builtin_fmin(__builtin_fmax(key[p], -1e300), 1e300), p * G + l);
+
+        // ---- groups ----
+        if constexpr (GROUPED) {
+            double *const mykeys = keys_smem + (wid * RPW + lane / G) * (G * P);
+#pragma unroll
+            for (int p = 0; p < P; ++p) mykeys[p * G + l] = key[p];
+            wave_sync();
+            double best = none, next = none;
+            if (l < a.groups)
+                for (int i = 0, c = l % a.group_size; i < a.group_size; ++i) {
+                    const double v = mykeys[l * a.group_size + c];
+                    next = __builtin_fmax(next, __builtin_fmin(best, v));
+                    best = __builtin_fmax(best, v);
+                    if (++c == a.group_size) c = 0;   // each group from another start: other banks
+                }
+            double total = best == none ? none : without_expert(best);
+            if (a.group_best > 1 && next != none) total += without_expert(next);
+            int better = 0;
+            for (int i = 0; i < a.groups; ++i) {
+                const double o = __shfl(total, first + i);
+                better += o > total || (o == total && i < l);
+            }
+            const unsigned long long kept = __ballot(l < a.groups && better < a.top_groups) >> first;
+            const unsigned magic = ((1u << 20) + a.group_size - 1) / a.group_size;   // e / group_size = e magic >> 20
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                if (!((kept >> (((unsigned)(p * G + l) * magic) >> 20)) & 1)) key[p] = none;
+            wave_sync();
+        }
+
+        // ---- the k best ----
+        sort_keys(key);
+        int chosen[G == 16 ? 2 : 1] = {};
+        for (int j = 0; j < a.k; ++j) {
+            const double top = all_reduce<G>(key[0], Max{});
+            const int e = top == none ? -1 : expert_of(top);
+            const bool here = key[0] == top && top != none;
+#pragma unroll
+            for (int p = 0; p + 1 < P; ++p) key[p] = here ? key[p + 1] : key[p];
+            if (here) key[P - 1] = none;
+            if (l == j) chosen[0] = e;
+            if constexpr (G == 16)
+                if (l + 16 == j) chosen[1] = e;
+        }
+
+        // ---- their weights ----
+        constexpr int NC = G == 16 ? 2 : 1;
+        float xs[NC], w[NC];
+        float mc = -__builtin_inff();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const bool there = live && l + c * G < a.k && chosen[c] >= 0;
+            xs[c] = there ? logit(a.x, a.dtype, row + chosen[c]) : -__builtin_inff();
+            mc = fmaxf(mc, xs[c]);
+        }
+        if (a.renorm) mc = all_reduce<G>(mc, Max{});
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const bool there = live && l + c * G < a.k && chosen[c] >= 0;
+            w[c] = there ? chosen_score(a.score, xs[c], a.renorm ? mc : a.score == SCORE_SOFTMAX ? m : 0.0f) : 0.0f;
+            sum += w[c];
+        }
+        if (a.renorm)
+            sum = all_reduce<G>(sum, Sum{});
+        else
+            sum = a.score == SCORE_SOFTMAX ? z : 1.0f;
+        const float by = sum > 0.0f ? a.scale / sum : 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int j = l + c * G;
+            if (live && j < a.k) {
+                const size_t at = (size_t)(t0 + r) * a.k + j;
+                a.indices[at] = chosen[c];
+                a.weights[at] = bad ? __builtin_nanf("") : w[c] * by;
+                if (a.counts && chosen[c] >= 0) atomicAdd(&count_smem[chosen[c]], 1);
+            }
+        }
+    }
+    if (a.counts) {
+        __syncthreads();
+        for (int e = tid; e < a.E; e += kRouteThreads) a.counts[(size_t)blockIdx.x * a.E + e] = count_smem[e];
+    }
+}
+
+// ------------------------------------------------------------------ sorting --
+
+// This block's slots of each expert, for sort_kernel.
+__global__ void __launch_bounds__(kRouteThreads)
+count_kernel(const int32_t *__restrict__ indices, int32_t *__restrict__ counts, int n, int E, int per_block) {
+    __shared__ int count_smem[kMaxExperts];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < E; e += kRouteThreads) count_smem[e] = 0;
+    __syncthreads();
+    const long long begin = (long long)blockIdx.x * per_block, end = min((long long)n, begin + per_block);
+    for (long long i = begin + tid; i < end; i += kRouteThreads) {
+        const int e = indices[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&count_smem[e], 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += kRouteThreads) counts[(size_t)blockIdx.x * E + e] = count_smem[e];
+}
+
+// Each block sorts its own slots into the rows that its experts' earlier blocks leave: every block adds
+// up all blocks' counts (before it: where it starts within an expert; all: the offsets), then its waves
+// take equal ranges of its slots in order. Slots of one expert in a wave's 64 find each other by ballots on
+// the bits of the expert's number, so that a row's place depends on its slot alone, and on no
+// atomic's order.
+__global__ void __launch_bounds__(kRouteThreads)
+sort_kernel(Sort a) {
+    __shared__ int place[kRouteWaves][kMaxExperts];
+    __shared__ int before_smem[kMaxExperts], total_smem[kMaxExperts], wave_sum[kRouteWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, E = a.E;
+    const int b = blockIdx.x;
+    // ---- counts of all blocks ----
+    for (int e = tid; e < E; e += kRouteThreads) before_smem[e] = total_smem[e] = 0;
+    for (int i = tid; i < kRouteWaves * kMaxExperts; i += kRouteThreads) (&place[0][0])[i] = 0;
+    __syncthreads();
+    if (a.blocks > 1) {
+        // Threads beyond the experts take other blocks of the same ones.
+        const int ways = max(kRouteThreads / E, 1), way = tid / E;
+        for (int e = E >= kRouteThreads ? tid : tid % E; e < E && (E >= kRouteThreads || way < ways); e += kRouteThreads) {
+            int before = 0, total = 0;
+            const int w = E >= kRouteThreads ? 0 : way;
+#pragma unroll 8
+            for (int i = w; i < a.blocks; i += ways) {
+                const int c = a.counts[(size_t)i * E + e];
+                total += c;
+                before += i < b ? c : 0;
+            }
+            atomicAdd(&before_smem[e], before);
+            atomicAdd(&total_smem[e], total);
+        }
+    }
+    const long long begin = (long long)b * a.per_block, end = min((long long)a.n, begin + a.per_block);
+    // A wave's range: whole rounds of 64.
+    const long long each = ((end - begin + kRouteThreads - 1) / kRouteThreads) * 64;
+    const long long wbegin = min(begin + wid * each, end), wend = min(wbegin + each, end);
+    for (long long i = wbegin + lane; i < wend; i += 64) {
+        const int e = a.indices[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&place[wid][e], 1);
+    }
+    __syncthreads();
+    // ---- offsets: a scan over the experts, and each wave's first row ----
+    constexpr int PER = kMaxExperts / kRouteThreads;
+    int own[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
+        own[i] = 0;
+        if (e < E) {
+            if (a.blocks > 1) {
+                own[i] = total_smem[e];
+            } else {
+                for (int w = 0; w < kRouteWaves; ++w) own[i] += place[w][e];
+            }
+        }
+        sum += own[i];
+    }
+    int upto = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 63) wave_sum[wid] = upto;
+    __syncthreads();
+    int offset = upto - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) {
+        if (w < wid) offset += wave_sum[w];
+        all += wave_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
+        if (e < E) {
+            if (b == 0) a.offsets[e] = offset;
+            int at = offset + before_smem[e];
+            for (int w = 0; w < kRouteWaves; ++w) {
+                const int c = place[w][e];
+                place[w][e] = at;
+                at += c;
+            }
+        }
+        offset += own[i];
+    }
+    if (b == 0 && tid == 0) a.offsets[E] = all;
+    __syncthreads();
+    // ---- each slot's row ----
+    const int bits = 32 - __clz(max(E - 1, 1));
+    for (long long i0 = wbegin; i0 < wend; i0 += 64) {
+        const long long i = i0 + lane;
+        int e = -1;
+        if (i < wend) e = a.indices[i];
+        const bool there = (unsigned)e < (unsigned)E;
+        unsigned long long same = __ballot(there);
+        for (int bit = 0; bit < bits; ++bit) {
+            const unsigned long long set = __ballot((e >> bit) & 1);
+            same &= (e >> bit) & 1 ? set : ~set;
+        }
+        int row = -1;
+        if (there) {
+            const int at = place[wid][e];
+            row = at + __popcll(same & ((1ull << lane) - 1));
+            if ((same >> lane) == 1) place[wid][e] = at + __popcll(same);   // its last slot
+        }
+        wave_sync();
+        if (i < wend) {
+            a.rows[i] = row;
+            if (a.slots && there) a.slots[row] = (int)i;
+        }
+    }
+    // Rows of no slot.
+    if (a.slots)
+        for (long long i = all + (long long)b * kRouteThreads + tid; i < a.n; i += (long long)a.blocks * kRouteThreads) a.slots[i] = -1;
+}
+
+// ----------------------------------------------------------------- gradient --
+
+struct RouteGrad {
+    const void *x;
+    const int32_t *indices;
+    const float *dw;
+    void *dx;
+    int T, E, k;
+    int score, renorm, dtype;
+    float scale;
+};
+
+__device__ __forceinline__ void store_logit(void *x, int dtype, size_t at, float v) {
+    if (dtype == DTYPE_F32)
+        ((float *)x)[at] = v;
+    else
+        ((uint16_t *)x)[at] = (uint16_t)(dtype == DT_BF16 ? pack2<DT_BF16>(v, 0.0f) : pack2<DT_F16>(v, 0.0f));
+}
+
+constexpr int kGradWaves = 4;
+
+// With g = scale dw and D the sum of (weight / scale) g over the chosen:
+//   softmax, renormalised:  dx_i = q_i (g_i - D) for the chosen, q the softmax over them; else 0
+//   softmax:                dx_e = p_e (g_e [chosen] - D) for every expert
+//   sigmoid, renormalised:  dx_i = q_i (1 - s_i) (g_i - D)
+//   sigmoid:                dx_i = g_i s_i (1 - s_i)
+// A row's chosen terms go through LDS to the lanes that hold the experts; reading and writing the logits
+// and their gradient once is what bounds it.
+template <int G, int P>
+__global__ void __launch_bounds__(kGradWaves * 64)
+route_grad_kernel(RouteGrad a) {
+    constexpr int RPW = 64 / G, NC = G == 16 ? 2 : 1;
+    __shared__ float smem[kGradWaves * RPW][G * P];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+    const int l = lane & (G - 1), first = lane - l;
+    const long long t = ((long long)linear_block() * kGradWaves + wid) * RPW + lane / G;
+    const bool live = t < a.T;
+    const size_t row = (size_t)(live ? t : 0) * a.E;
+    float *const terms = smem[wid * RPW + lane / G];
+#pragma unroll
+    for (int p = 0; p < P; ++p) terms[p * G + l] = 0.0f;
+    int e[NC];
+    float g[NC], xs[NC], mc = -__builtin_inff();
+    bool some = false;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int j = l + c * G;
+        e[c] = -1;
+        if (live && j < a.k) e[c] = a.indices[(size_t)t * a.k + j];
+        if ((unsigned)e[c] >= (unsigned)a.E) e[c] = -1;
+        const bool there = e[c] >= 0;
+        g[c] = there ? a.scale * a.dw[(size_t)t * a.k + j] : 0.0f;
+        xs[c] = there ? logit(a.x, a.dtype, row + e[c]) : -__builtin_inff();
+        mc = fmaxf(mc, xs[c]);
+        some |= there;
+    }
+    some = any_of<G>(some, first);
+    const bool dense = a.score == SCORE_SOFTMAX && !a.renorm;
+    float x[P], m = -__builtin_inff(), z = 0.0f;
+    if (dense) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            x[p] = live && p * G + l < a.E ? logit(a.x, a.dtype, row + p * G + l) : -__builtin_inff();
+            m = fmaxf(m, x[p]);
+        }
+        m = all_reduce<G>(m, Max{});
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            x[p] = x[p] == -__builtin_inff() ? 0.0f : expf(x[p] - m);
+            z += x[p];
+        }
+        z = all_reduce<G>(z, Sum{});
+    } else {
+        m = all_reduce<G>(mc, Max{});
+    }
+    float q[NC], sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        q[c] = e[c] >= 0 ? chosen_score(a.score, xs[c], a.renorm || dense ? m : 0.0f) : 0.0f;
+        sum += q[c];
+    }
+    sum = all_reduce<G>(sum, Sum{});
+    const float by = dense ? 1.0f / z : a.renorm ? 1.0f / sum : 1.0f;
+    float d = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        q[c] *= by;
+        if (e[c] >= 0) d = fmaf(q[c], g[c], d);
+    }
+    d = dense || a.renorm ? all_reduce<G>(d, Sum{}) : 0.0f;
+    wave_sync();
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        if (e[c] < 0) continue;
+        float v = g[c];
+        if (!dense) v = q[c] * (v - d);
+        if (a.score == SCORE_SIGMOID) v *= 1.0f / (1.0f + expf(xs[c]));
+        atomicAdd(&terms[e[c]], v);   // a repeated expert's terms add up
+    }
+    wave_sync();
+    if (!live) return;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int at = p * G + l;
+        float v = terms[at];
+        if (dense) v = some ? x[p] * by * (v - d) : 0.0f;
+        if (at < a.E) store_logit(a.dx, a.dtype, row + at, v);
+    }
+}
+
+}  // namespace gbm
