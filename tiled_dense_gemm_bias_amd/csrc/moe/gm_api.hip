@@ -91,14 +91,17 @@ bool bad_route(int64_t T, int64_t E, int64_t k) {
 
 // ------------------------------------------------------------------- sorting --
 
-// Slots sorted by one workgroup, beyond which each block of a larger grid counts its own first.
+// Slots that one workgroup sorts, beyond which each block of a larger grid counts its own first; blocks of such a grid
+// (each adds up all blocks' counts).
 constexpr int kBlockSlots = 2048, kMaxBlocks = 256;
 
-// Tokens a block and blocks: at most 256 blocks (each adds up all blocks' counts) of at least 64 tokens.
-void sort_shape(int64_t T, int64_t k, int *tokens, int *blocks) {
-    const int64_t least = T * k <= kBlockSlots ? T : 64;
+// Tokens a block: as few as 256 blocks leave, in whole sixteens (four waves of a routing block with up to 256 experts;
+// a wave's pass takes some 10 us whatever the others do, so that few tokens belong on many CUs).
+constexpr int kLeastTokens = 16;
+
+void sort_shape(int64_t T, int64_t E, int64_t k, int *tokens, int *blocks) {
     int64_t per = (T + kMaxBlocks - 1) / kMaxBlocks;
-    per = per < least ? least : (per + 63) / 64 * 64;
+    per = T * k <= kBlockSlots ? T : (per + kLeastTokens - 1) / kLeastTokens * kLeastTokens;
     if (per < 1) per = 1;
     *tokens = (int)per;
     *blocks = T ? (int)((T + per - 1) / per) : 1;
@@ -106,29 +109,34 @@ void sort_shape(int64_t T, int64_t k, int *tokens, int *blocks) {
 
 size_t sort_bytes(int64_t T, int64_t E, int64_t k) {
     int tokens, blocks;
-    sort_shape(T, k, &tokens, &blocks);
-    return blocks > 1 ? size3(blocks, E, 4) : 0;
+    sort_shape(T, E, k, &tokens, &blocks);
+    return blocks > 1 ? size3(blocks, gbm::count_pitch((int)E), 4) : 0;
 }
 
-hipError_t launch_sort(const int32_t *indices, const int32_t *counts, int32_t *offsets, int32_t *rows, int32_t *slots, int64_t T,
-                       int64_t E, int64_t k) {
+gbm::Sort sort_of(const int32_t *indices, const void *counts, int32_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int64_t E,
+                  int64_t k) {
     int tokens, blocks;
-    sort_shape(T, k, &tokens, &blocks);
-    gbm::Sort s = {indices, counts, offsets, rows, slots, (int)(T * k), (int)E, (int)(tokens * k), blocks};
-    return gbm::launch(gbm::sort_kernel, dim3(blocks), dim3(gbm::kRouteThreads), t_stream, s);
+    sort_shape(T, E, k, &tokens, &blocks);
+    return {indices, (const int32_t *)counts, offsets, rows, slots, (int)(T * k), (int)E, (int)(tokens * k), blocks};
+}
+
+hipError_t launch_sort(const gbm::Sort &s) {
+    return gbm::launch(s.E <= 256 ? gbm::sort_kernel<256> : gbm::sort_kernel<1024>, dim3(s.blocks), dim3(gbm::kRouteThreads), t_stream, s);
 }
 
 template <bool GROUPED>
-hipError_t launch_route(const gbm::Route &a, int64_t blocks) {
-    const dim3 grid = gba::tile_grid(blocks), block(gbm::kRouteThreads);
-    void (*kernel)(gbm::Route) = a.E <= 16    ? gbm::route_kernel<16, 1, GROUPED>
-                                 : a.E <= 32  ? gbm::route_kernel<16, 2, GROUPED>
-                                 : a.E <= 64  ? gbm::route_kernel<16, 4, GROUPED>
-                                 : a.E <= 128 ? gbm::route_kernel<16, 8, GROUPED>
-                                 : a.E <= 256 ? gbm::route_kernel<16, 16, GROUPED>
-                                 : a.E <= 512 ? gbm::route_kernel<64, 8, GROUPED>
-                                              : gbm::route_kernel<64, 16, GROUPED>;
-    return gbm::launch(kernel, grid, block, t_stream, a);
+hipError_t launch_route(const gbm::Route &a, const gbm::Sort &s, int64_t blocks) {
+    const int waves = (a.tokens * (a.E <= 256 ? 16 : 64) + 63) / 64;   // of one pass
+    const dim3 grid = gba::tile_grid(blocks);
+    const dim3 block(s.indices || waves > gbm::kRouteWaves ? gbm::kRouteThreads : waves * 64);
+    void (*kernel)(gbm::Route, gbm::Sort) = a.E <= 16    ? gbm::route_kernel<16, 1, GROUPED>
+                                            : a.E <= 32  ? gbm::route_kernel<16, 2, GROUPED>
+                                            : a.E <= 64  ? gbm::route_kernel<16, 4, GROUPED>
+                                            : a.E <= 128 ? gbm::route_kernel<16, 8, GROUPED>
+                                            : a.E <= 256 ? gbm::route_kernel<16, 16, GROUPED>
+                                            : a.E <= 512 ? gbm::route_kernel<64, 8, GROUPED>
+                                                         : gbm::route_kernel<64, 16, GROUPED>;
+    return gbm::launch(kernel, grid, block, t_stream, a, s);
 }
 
 // ------------------------------------------------------------------- products --
@@ -216,17 +224,16 @@ int moe_route(const void *logits, const float *bias, int32_t *indices, float *we
                           {offsets, size3(E + 1, 4, 1), sort, true, 4},
                           {rows, size3(T, k, 4), sort, true, 4},
                           {slots, size3(T, k, 4), false, true, 4},
-                          {workspace, workspace_bytes, false, true, 4}};
+                          {workspace, workspace_bytes, false, true, 16}};
     int s = check_spans(spans);
     if (s) return s;
     if (sort && workspace_bytes < sort_bytes(T, E, k)) return GBA_ERR_SCRATCH;
     if (sort && sort_bytes(T, E, k) && !workspace) return GBA_ERR_NULL;
     if (T == 0 && !sort) return GBA_OK;
     if ((s = check_device())) return s;
-    int tokens, blocks;
-    sort_shape(T, k, &tokens, &blocks);
-    const bool counted = sort && blocks > 1;
+    gbm::Sort order = sort_of(indices, workspace, offsets, rows, slots, T, E, k);
     if (T > 0) {
+        const bool counted = sort && order.blocks > 1;
         gbm::Route a = {};
         a.x = logits;
         a.bias = bias;
@@ -244,13 +251,15 @@ int moe_route(const void *logits, const float *bias, int32_t *indices, float *we
         a.renorm = (flags & GBM_RENORMALIZE) != 0;
         a.dtype = dtype;
         a.scale = scale;
-        // Without counts a block is one pass over its rows.
-        const int pass = gbm::kRouteWaves * (E <= 256 ? 4 : 1);
-        a.tokens = counted ? tokens : pass;
+        // One pass of one block of up to 256 experts: it sorts as well.
+        const bool fused = sort && !counted && E <= 256 && T <= gbm::kRouteWaves * 4;
+        a.tokens = fused ? (int)T : counted ? order.per_block / (int)k : kLeastTokens;
+        gbm::Sort inside = order;
+        if (!fused) inside.indices = nullptr;
         const int64_t n = (T + a.tokens - 1) / a.tokens;
-        if ((s = hip_result(groups > top_groups ? launch_route<true>(a, n) : launch_route<false>(a, n)))) return s;
+        if ((s = hip_result(groups > top_groups ? launch_route<true>(a, inside, n) : launch_route<false>(a, inside, n))) || fused) return s;
     }
-    return sort ? hip_result(launch_sort(indices, (const int32_t *)workspace, offsets, rows, slots, T, E, k)) : GBA_OK;
+    return sort ? hip_result(launch_sort(order)) : GBA_OK;
 }
 
 int moe_route_grad(const void *logits, const int32_t *indices, const float *dweights, void *dlogits, int64_t T, int64_t E, int64_t k,
@@ -287,20 +296,19 @@ int moe_sort(const int32_t *indices, int32_t *offsets, int32_t *rows, int32_t *s
                           {offsets, size3(E + 1, 4, 1), true, true, 4},
                           {rows, size3(T, k, 4), true, true, 4},
                           {slots, size3(T, k, 4), false, true, 4},
-                          {workspace, workspace_bytes, false, true, 4}};
+                          {workspace, workspace_bytes, false, true, 16}};
     int s = check_spans(spans);
     if (s) return s;
     if (workspace_bytes < sort_bytes(T, E, k)) return GBA_ERR_SCRATCH;
     if (sort_bytes(T, E, k) && !workspace) return GBA_ERR_NULL;
     if ((s = check_device())) return s;
-    int tokens, blocks;
-    sort_shape(T, k, &tokens, &blocks);
-    if (blocks > 1) {
-        s = hip_result(gbm::launch(gbm::count_kernel, dim3(blocks), dim3(gbm::kRouteThreads), t_stream, indices, (int32_t *)workspace,
-                                   (int)(T * k), (int)E, (int)(tokens * k)));
+    const gbm::Sort order = sort_of(indices, workspace, offsets, rows, slots, T, E, k);
+    if (order.blocks > 1) {
+        s = hip_result(gbm::launch(gbm::count_kernel, dim3(order.blocks), dim3(gbm::kRouteThreads), t_stream, indices, (int32_t *)workspace,
+                                   order.n, order.E, order.per_block));
         if (s) return s;
     }
-    return hip_result(launch_sort(indices, (const int32_t *)workspace, offsets, rows, slots, T, E, k));
+    return hip_result(launch_sort(order));
 }
 
 // Tokens, slots, columns and experts' rows of the moves.

@@ -16,7 +16,4 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// e^d for d <= 0, in 64 bits.
-__device__ __forceinline__ double exp_to_one(double d) { return exp(d); }
-
 }  // namespace gbm

@@ -8,14 +8,15 @@
 // scores' order, exact in every type); otherwise it is score + bias in 64 bits, cut to 42: values
 // that differ by less count as ties. (In 32 bits about one in 10^5 rows of 256 experts chose
 // another expert than the formulas do.) A lane sorts its own values once, then k rounds take the
-// largest of the G first ones and move up the winner's list.
+// largest of the G first ones and move up the winner's list. Keys of 32 bits, with the rows done again in 64 whose
+// neighbours 32 cannot tell apart, take half the instructions, but the few waves that do both end no sooner.
 //
 // Groups: the keys go through LDS, where lane g scans group g for its best one or two.
 //
 // The weights are computed from the chosen logits in 32 bits, renormalised sigmoid weights as
 // ratios that do not underflow together: s_i e^-min(m, 0), m the largest chosen logit.
 //
-// What bounds it: instructions. 16384 rows of 256 fp32 logits, k = 8, are 17 MB (3.3 us at 5.1 TB/s).
+// What bounds it: instructions and latency. 16384 rows of 256 fp32 logits, k = 8, are 17 MB (3.3 us at 5.1 TB/s).
 #pragma once
 
 #include "gm_common.hpp"
@@ -23,7 +24,7 @@
 namespace gbm {
 
 constexpr int kMaxExperts = 1024, kMaxTop = 32, kMaxGroups = 16;
-constexpr int kRouteWaves = 8, kRouteThreads = kRouteWaves * 64;
+constexpr int kRouteWaves = 16, kRouteThreads = kRouteWaves * 64;
 enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
 
 struct Route {
@@ -31,7 +32,8 @@ struct Route {
     const float *bias;     // [E] or null
     int32_t *indices;      // [T][k]
     float *weights;        // [T][k]
-    int32_t *counts;       // [blocks][E]: this block's slots of each expert (null: no sort follows)
+    int32_t *counts;       // [blocks][pitch]: this block's slots of each expert (null: no sort_kernel with several
+                           // blocks follows)
     int T, E, k;
     int groups, top_groups, group_best, group_size;
     int score, renorm, dtype;
@@ -39,16 +41,17 @@ struct Route {
     int tokens;            // per block
 };
 
-// One slot array sorted by expert: see sort_block.
+// Slots to be sorted by expert: see sort_block.
 struct Sort {
     const int32_t *indices;   // [T k]
-    const int32_t *counts;    // [blocks][E]
+    const int32_t *counts;    // [blocks][pitch]
     int32_t *offsets;         // [E + 1]
     int32_t *rows;            // [T k]
     int32_t *slots;           // [T k] or null
     int n, E;                 // slots, experts
     int per_block, blocks;    // slots a block
 };
+__host__ __device__ constexpr int count_pitch(int E) { return (E + 3) & ~3; }   // a block's counts, in whole 16 bytes
 
 constexpr unsigned long long kExpertBits = 1023;
 
@@ -128,186 +131,6 @@ __device__ __forceinline__ void sort_keys(double (&v)[P]) {
                     }
 }
 
-__device__ __forceinline__ float logit(const void *x, int dtype, size_t at) {
-    if (dtype == DTYPE_F32) return ((const float *)x)[at];
-    const uint32_t h = ((const uint16_t *)x)[at];
-    return dtype == DT_BF16 ? to_f32<DT_BF16>(h) : to_f32<DT_F16>(h);
-}
-
-// t_i of the chosen logits (t_i / sum t is the renormalised weight) and, for sigmoid scores,
-// s_i e^-min(m, 0) with m the largest: no common underflow.
-__device__ __forceinline__ float chosen_score(int score, float x, float m) {
-    if (score == SCORE_SOFTMAX) return expf(x - m);
-    return x >= 0 ? 1.0f / (1.0f + expf(-x)) : expf(x - fminf(m, 0.0f)) / (1.0f + expf(x));
-}
-
-template <int G, int P, bool GROUPED>
-__global__ void __launch_bounds__(kRouteThreads)
-route_kernel(Route a) {
-    constexpr int RPW = 64 / G;                        // rows a wave
-    constexpr int RPB = kRouteWaves * RPW;             // rows a block and pass
-    __shared__ double keys_smem[GROUPED ? RPB * G * P : 1];
-    __shared__ int count_smem[kMaxExperts];
-    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    const int l = lane & (G - 1), first = lane - l;
-    const double none = -__builtin_inf();
-    const long long t0 = (long long)linear_block() * a.tokens;
-    const int mine = (int)min((long long)a.tokens, a.T - t0);
-
-    if (a.counts) {
-        for (int e = tid; e < a.E; e += kRouteThreads) count_smem[e] = 0;
-        __syncthreads();
-    }
-    for (int pass = 0; pass < mine; pass += RPB) {
-        const int r = pass + wid * RPW + lane / G;
-        const bool live = r < mine;
-        const size_t row = (size_t)(t0 + (live ? r : 0)) * a.E;
-        float x[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int e = p * G + l;
-            x[p] = live && e < a.E ? logit(a.x, a.dtype, row + e) : -__builtin_inff();
-        }
-        // ---- values ----
-        const bool scored = a.bias != nullptr || (GROUPED && a.group_best > 1);
-        float m = -__builtin_inff();
-        bool bad = false;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            m = fmaxf(m, x[p]);
-            bad |= x[p] != x[p];
-        }
-        float z = 0.0f;      // softmax: the sum of e^(x - m)
-        double key[P];
-        if (a.score == SCORE_SOFTMAX) {
-            m = all_reduce<G>(m, Max{});
-            bad |= m == __builtin_inff();
-        }
-        if (scored) {
-            double total = 1.0;
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                if (a.score == SCORE_SOFTMAX)
-                    key[p] = x[p] == -__builtin_inff() ? 0.0 : exp_to_one((double)x[p] - (double)m);
-                else
-                    key[p] = 1.0 / (1.0 + exp(-(double)x[p]));
-            }
-            if (a.score == SCORE_SOFTMAX) {
-                double sum = 0.0;
-#pragma unroll
-                for (int p = 0; p < P; ++p) sum += key[p];
-                sum = all_reduce<G>(sum, Sum{});
-                z = (float)sum;
-                total = sum > 0.0 ? 1.0 / sum : 0.0;
-            }
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int e = p * G + l;
-                float b = 0.0f;
-                if (a.bias && e < a.E) b = a.bias[e];
-                bad |= b != b;
-                if (b == -__builtin_inff()) x[p] = b;   // never chosen
-                key[p] = key[p] * total + (double)b;
-            }
-        } else {
-            if (a.score == SCORE_SOFTMAX && !a.renorm) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int p = 0; p < P; ++p) sum += x[p] == -__builtin_inff() ? 0.0f : expf(x[p] - m);
-                z = all_reduce<G>(sum, Sum{});
-            }
-#pragma unroll
-            for (int p = 0; p < P; ++p) key[p] = (double)x[p];
-        }
-        bad = any_of<G>(bad, first);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            key[p] = bad || x[p] == -__builtin_inff() ? none : key_of(__builtin_fmin(__builtin_fmax(key[p], -1e300), 1e300), p * G + l);
-
-        // ---- groups ----
-        if constexpr (GROUPED) {
-            double *const mykeys = keys_smem + (wid * RPW + lane / G) * (G * P);
-#pragma unroll
-            for (int p = 0; p < P; ++p) mykeys[p * G + l] = key[p];
-            wave_sync();
-            double best = none, next = none;
-            if (l < a.groups)
-                for (int i = 0, c = l % a.group_size; i < a.group_size; ++i) {
-                    const double v = mykeys[l * a.group_size + c];
-                    next = __builtin_fmax(next, __builtin_fmin(best, v));
-                    best = __builtin_fmax(best, v);
-                    if (++c == a.group_size) c = 0;   // each group from another start: other banks
-                }
-            double total = best == none ? none : without_expert(best);
-            if (a.group_best > 1 && next != none) total += without_expert(next);
-            int better = 0;
-            for (int i = 0; i < a.groups; ++i) {
-                const double o = __shfl(total, first + i);
-                better += o > total || (o == total && i < l);
-            }
-            const unsigned long long kept = __ballot(l < a.groups && better < a.top_groups) >> first;
-            const unsigned magic = ((1u << 20) + a.group_size - 1) / a.group_size;   // e / group_size = e magic >> 20
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                if (!((kept >> (((unsigned)(p * G + l) * magic) >> 20)) & 1)) key[p] = none;
-            wave_sync();
-        }
-
-        // ---- the k best ----
-        sort_keys(key);
-        int chosen[G == 16 ? 2 : 1] = {};
-        for (int j = 0; j < a.k; ++j) {
-            const double top = all_reduce<G>(key[0], Max{});
-            const int e = top == none ? -1 : expert_of(top);
-            const bool here = key[0] == top && top != none;
-#pragma unroll
-            for (int p = 0; p + 1 < P; ++p) key[p] = here ? key[p + 1] : key[p];
-            if (here) key[P - 1] = none;
-            if (l == j) chosen[0] = e;
-            if constexpr (G == 16)
-                if (l + 16 == j) chosen[1] = e;
-        }
-
-        // ---- their weights ----
-        constexpr int NC = G == 16 ? 2 : 1;
-        float xs[NC], w[NC];
-        float mc = -__builtin_inff();
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const bool there = live && l + c * G < a.k && chosen[c] >= 0;
-            xs[c] = there ? logit(a.x, a.dtype, row + chosen[c]) : -__builtin_inff();
-            mc = fmaxf(mc, xs[c]);
-        }
-        if (a.renorm) mc = all_reduce<G>(mc, Max{});
-        float sum = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const bool there = live && l + c * G < a.k && chosen[c] >= 0;
-            w[c] = there ? chosen_score(a.score, xs[c], a.renorm ? mc : a.score == SCORE_SOFTMAX ? m : 0.0f) : 0.0f;
-            sum += w[c];
-        }
-        if (a.renorm)
-            sum = all_reduce<G>(sum, Sum{});
-        else
-            sum = a.score == SCORE_SOFTMAX ? z : 1.0f;
-        const float by = sum > 0.0f ? a.scale / sum : 0.0f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int j = l + c * G;
-            if (live && j < a.k) {
-                const size_t at = (size_t)(t0 + r) * a.k + j;
-                a.indices[at] = chosen[c];
-                a.weights[at] = bad ? __builtin_nanf("") : w[c] * by;
-                if (a.counts && chosen[c] >= 0) atomicAdd(&count_smem[chosen[c]], 1);
-            }
-        }
-    }
-    if (a.counts) {
-        __syncthreads();
-        for (int e = tid; e < a.E; e += kRouteThreads) a.counts[(size_t)blockIdx.x * a.E + e] = count_smem[e];
-    }
-}
-
 // ------------------------------------------------------------------ sorting --
 
 // This block's slots of each expert, for sort_kernel.
@@ -315,7 +138,7 @@ __global__ void __launch_bounds__(kRouteThreads)
 count_kernel(const int32_t *__restrict__ indices, int32_t *__restrict__ counts, int n, int E, int per_block) {
     __shared__ int count_smem[kMaxExperts];
     const int tid = threadIdx.x;
-    for (int e = tid; e < E; e += kRouteThreads) count_smem[e] = 0;
+    for (int e = tid; e < count_pitch(E); e += kRouteThreads) count_smem[e] = 0;
     __syncthreads();
     const long long begin = (long long)blockIdx.x * per_block, end = min((long long)n, begin + per_block);
     for (long long i = begin + tid; i < end; i += kRouteThreads) {
@@ -323,38 +146,42 @@ count_kernel(const int32_t *__restrict__ indices, int32_t *__restrict__ counts, 
         if ((unsigned)e < (unsigned)E) atomicAdd(&count_smem[e], 1);
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kRouteThreads) counts[(size_t)blockIdx.x * E + e] = count_smem[e];
+    for (int e = tid; e < count_pitch(E); e += kRouteThreads) counts[(size_t)blockIdx.x * count_pitch(E) + e] = count_smem[e];
 }
 
-// Each block sorts its own slots into the rows that its experts' earlier blocks leave: every block adds
+// Block b sorts its own slots into the rows that its experts' earlier blocks leave: every block adds
 // up all blocks' counts (before it: where it starts within an expert; all: the offsets), then its waves
 // take equal ranges of its slots in order. Slots of one expert in a wave's 64 find each other by ballots on
 // the bits of the expert's number, so that a row's place depends on its slot alone, and on no
-// atomic's order.
-__global__ void __launch_bounds__(kRouteThreads)
-sort_kernel(Sort a) {
-    __shared__ int place[kRouteWaves][kMaxExperts];
-    __shared__ int before_smem[kMaxExperts], total_smem[kMaxExperts], wave_sum[kRouteWaves];
+// atomic's order. place: LDS, for up to EP experts.
+template <int EP>
+__device__ __forceinline__ void sort_block(const Sort &a, int b, int (*place)[EP]) {
+    __shared__ int before_smem[EP], total_smem[EP], wave_sum[kRouteWaves];
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, E = a.E;
-    const int b = blockIdx.x;
     // ---- counts of all blocks ----
-    for (int e = tid; e < E; e += kRouteThreads) before_smem[e] = total_smem[e] = 0;
-    for (int i = tid; i < kRouteWaves * kMaxExperts; i += kRouteThreads) (&place[0][0])[i] = 0;
+    for (int e = tid; e < EP; e += kRouteThreads) before_smem[e] = total_smem[e] = 0;
+    for (int i = tid; i < kRouteWaves * EP; i += kRouteThreads) (&place[0][0])[i] = 0;
     __syncthreads();
     if (a.blocks > 1) {
-        // Threads beyond the experts take other blocks of the same ones.
-        const int ways = max(kRouteThreads / E, 1), way = tid / E;
-        for (int e = E >= kRouteThreads ? tid : tid % E; e < E && (E >= kRouteThreads || way < ways); e += kRouteThreads) {
-            int before = 0, total = 0;
-            const int w = E >= kRouteThreads ? 0 : way;
-#pragma unroll 8
-            for (int i = w; i < a.blocks; i += ways) {
-                const int c = a.counts[(size_t)i * E + e];
+        // Four experts a thread; the threads past the last four take other blocks of the first ones.
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        const int quads = count_pitch(E) / 4, ways = kRouteThreads / quads;
+        const int q = tid % quads, way = tid / quads;
+        if (way < ways) {
+            i32x4 before = {0, 0, 0, 0}, total = {0, 0, 0, 0};
+            const i32x4 *const counts = reinterpret_cast<const i32x4 *>(a.counts) + q;
+#pragma unroll 16
+            for (int i = way; i < a.blocks; i += ways) {
+                const i32x4 c = counts[(size_t)i * quads];
                 total += c;
-                before += i < b ? c : 0;
+                before += i < b ? c : i32x4{0, 0, 0, 0};
             }
-            atomicAdd(&before_smem[e], before);
-            atomicAdd(&total_smem[e], total);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * q + i < E) {
+                    atomicAdd(&before_smem[4 * q + i], before[i]);
+                    atomicAdd(&total_smem[4 * q + i], total[i]);
+                }
         }
     }
     const long long begin = (long long)b * a.per_block, end = min((long long)a.n, begin + a.per_block);
@@ -366,23 +193,18 @@ sort_kernel(Sort a) {
         if ((unsigned)e < (unsigned)E) atomicAdd(&place[wid][e], 1);
     }
     __syncthreads();
-    // ---- offsets: a scan over the experts, and each wave's first row ----
-    constexpr int PER = kMaxExperts / kRouteThreads;
-    int own[PER], sum = 0;
+    // ---- offsets: a scan over the experts (one a thread), and each wave's first row ----
+    static_assert(EP <= kRouteThreads, "one expert a thread");
+    int own = 0;
+    if (tid < E) {
+        if (a.blocks > 1) {
+            own = total_smem[tid];
+        } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = tid * PER + i;
-        own[i] = 0;
-        if (e < E) {
-            if (a.blocks > 1) {
-                own[i] = total_smem[e];
-            } else {
-                for (int w = 0; w < kRouteWaves; ++w) own[i] += place[w][e];
-            }
+            for (int w = 0; w < kRouteWaves; ++w) own += place[w][tid];
         }
-        sum += own[i];
     }
-    int upto = sum;
+    int upto = own;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int o = __shfl_up(upto, d);
@@ -390,25 +212,21 @@ sort_kernel(Sort a) {
     }
     if (lane == 63) wave_sum[wid] = upto;
     __syncthreads();
-    int offset = upto - sum, all = 0;
+    int offset = upto - own, all = 0;
 #pragma unroll
     for (int w = 0; w < kRouteWaves; ++w) {
         if (w < wid) offset += wave_sum[w];
         all += wave_sum[w];
     }
+    if (tid < E) {
+        if (b == 0) a.offsets[tid] = offset;
+        int at = offset + before_smem[tid];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = tid * PER + i;
-        if (e < E) {
-            if (b == 0) a.offsets[e] = offset;
-            int at = offset + before_smem[e];
-            for (int w = 0; w < kRouteWaves; ++w) {
-                const int c = place[w][e];
-                place[w][e] = at;
-                at += c;
-            }
+        for (int w = 0; w < kRouteWaves; ++w) {
+            const int c = place[w][tid];
+            place[w][tid] = at;
+            at += c;
         }
-        offset += own[i];
     }
     if (b == 0 && tid == 0) a.offsets[E] = all;
     __syncthreads();
@@ -441,6 +259,290 @@ sort_kernel(Sort a) {
         for (long long i = all + (long long)b * kRouteThreads + tid; i < a.n; i += (long long)a.blocks * kRouteThreads) a.slots[i] = -1;
 }
 
+template <int EP>
+__global__ void __launch_bounds__(kRouteThreads)
+sort_kernel(Sort a) {
+    __shared__ int place[kRouteWaves][EP];
+    sort_block<EP>(a, blockIdx.x, place);
+}
+
+// ------------------------------------------------------------------ routing --
+
+__device__ __forceinline__ float logit(const void *x, int dtype, size_t at) {
+    if (dtype == DTYPE_F32) return ((const float *)x)[at];
+    const uint32_t h = ((const uint16_t *)x)[at];
+    return dtype == DT_BF16 ? to_f32<DT_BF16>(h) : to_f32<DT_F16>(h);
+}
+// A row's values, `none` past the last. G P experts need no bounds, and a lane's loads then differ by constants only.
+template <int G, int P, class T>
+__device__ __forceinline__ void load_row(const T *x, int l, int E, T none, T (&v)[P]) {
+    const T *const mine = x + l;
+    if (E == G * P) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) v[p] = mine[p * G];
+        return;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        v[p] = none;
+        if (p * G + l < E) v[p] = mine[p * G];
+    }
+}
+template <int G, int P>
+__device__ __forceinline__ void load_logits(const void *x, int dtype, size_t row, int l, int E, float (&v)[P]) {
+    if (dtype == DTYPE_F32) {
+        load_row<G, P>((const float *)x + row, l, E, -__builtin_inff(), v);
+        return;
+    }
+    uint16_t h[P];
+    load_row<G, P>((const uint16_t *)x + row, l, E, (uint16_t)(dtype == DT_BF16 ? 0xff80 : 0xfc00), h);
+#pragma unroll
+    for (int p = 0; p < P; ++p) v[p] = dtype == DT_BF16 ? to_f32<DT_BF16>(h[p]) : to_f32<DT_F16>(h[p]);
+}
+
+// e^d for d <= 0: the hardware's 2^t with t = d log2 e, what t's rounding lost put back. Within 2^-22; 0 below 2^-126.
+__device__ __forceinline__ float exp_neg(float d) {
+    const float c = fmaxf(d, -200.0f);   // (-inf: no NaN)
+    const float t = c * 1.4426950408889634f;
+    const float r = fmaf(c, 1.9259629911e-8f, fmaf(c, 1.4426950408889634f, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0.6931471805599453f, e);
+}
+
+// t_i of the chosen logits (t_i / sum t is the renormalised weight) and, for sigmoid scores,
+// s_i e^-min(m, 0) with m the largest: no common underflow.
+__device__ __forceinline__ float chosen_score(int score, float x, float m) {
+    if (score == SCORE_SOFTMAX) return exp_neg(x - m);
+    const float t = exp_neg(-fabsf(x));
+    return (x >= 0 ? 1.0f : m >= 0 ? t : exp_neg(x - m)) / (1.0f + t);
+}
+
+// e^d for d <= 0 in 64 bits, within 2^-46 (the keys keep 42): d = n ln 2 + r, |r| <= ln 2 / 2, and e^r by its series up
+// to r^11 (the next term is 2^-47).
+__device__ __forceinline__ double exp_neg(double d) {
+    const double c = __builtin_fmax(d, -800.0);
+    const double n = __builtin_rint(c * 1.4426950408889634);
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -6.93147180369123816490e-01, c));
+    double p = 1.0 / 39916800.0;
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __builtin_ldexp(p, (int)n);
+}
+// 1 / d for 1 <= d <= 2^10, within 2^-50: the hardware's 2^-14 or better, twice by Newton's step.
+__device__ __forceinline__ double reciprocal(double d) {
+    double q = __builtin_amdgcn_rcp(d);
+    q = fma(fma(-d, q, 1.0), q, q);
+    q = fma(fma(-d, q, 1.0), q, q);
+    return fma(fma(-d, q, 1.0), q, q);
+}
+
+// Takes the largest of the row's first keys, `none` if there is none, and moves up that lane's list, of which the first
+// D are needed.
+template <int G, int D, int P>
+__device__ __forceinline__ double take_best(double (&key)[P], double none) {
+    const double top = all_reduce<G>(key[0], Max{});
+    const bool here = key[0] == top;   // (where there is none left all lists are empty)
+    constexpr int N = D < P ? D : P;
+#pragma unroll
+    for (int p = 0; p + 1 < N; ++p) key[p] = here ? key[p + 1] : key[p];
+    key[N - 1] = here ? none : key[N - 1];
+    return top;
+}
+
+// s.indices: the one block has all tokens and sorts their slots too.
+template <int G, int P, bool GROUPED>
+__global__ void __launch_bounds__(kRouteThreads)
+route_kernel(Route a, Sort s) {
+    constexpr int RPW = 64 / G;                        // rows a wave
+    constexpr int NC = G == 16 ? 2 : 1, EP = G * P;
+    const int threads = blockDim.x, RPB = threads / G;  // rows a block and pass
+    constexpr bool FUSE = EP <= 256;
+    // The rows' keys, where groups are limited; after the rows the sort's places.
+    constexpr int KEYS = GROUPED ? kRouteWaves * RPW * EP * 8 : 16, PLACES = FUSE ? kRouteWaves * EP * 4 : 16;
+    __shared__ __attribute__((aligned(16))) char smem[KEYS > PLACES ? KEYS : PLACES];
+    __shared__ int count_smem[EP];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sub = lane / G;
+    const int l = lane & (G - 1), first = lane - l;
+    const double none = -__builtin_inf();
+    const long long t0 = (long long)linear_block() * a.tokens;
+    const int mine = (int)min((long long)a.tokens, a.T - t0);
+
+    if (a.counts) {
+        for (int e = tid; e < a.E; e += threads) count_smem[e] = 0;
+        __syncthreads();
+    }
+    for (int pass = 0; pass < mine; pass += RPB) {
+        const int rr = pass + wid * RPW + sub;
+        const bool live = rr < mine;
+        const size_t row = (size_t)(t0 + (live ? rr : 0)) * a.E;
+        float x[P];
+        load_logits<G, P>(a.x, a.dtype, row, l, a.E, x);
+        const bool softmax = a.score == SCORE_SOFTMAX;
+        const bool scored = a.bias != nullptr || (GROUPED && a.group_best > 1);
+        float b[P];
+        if (a.bias) {
+            load_row<G, P>(a.bias, l, a.E, 0.0f, b);
+        } else {
+#pragma unroll
+            for (int p = 0; p < P; ++p) b[p] = 0.0f;
+        }
+        float m = -__builtin_inff();
+        bool bad = false;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            m = fmaxf(m, x[p]);
+            bad |= x[p] != x[p] || b[p] != b[p];
+            b[p] = fminf(b[p], 3.4e38f);   // finite, beside a masked logit's -inf
+        }
+        if (softmax) {
+            m = all_reduce<G>(m, Max{});
+            bad |= m == __builtin_inff();
+        }
+        bad = any_of<G>(bad, first);
+
+        // ---- keys ----
+        __builtin_amdgcn_sched_barrier(0);
+        float z = 0.0f;      // softmax: the sum of e^(x - m)
+        double key[P];
+        if (scored) {
+            double sum = 0.0;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const double t = exp_neg(softmax ? (double)x[p] - (double)m : -__builtin_fabs((double)x[p]));
+                key[p] = softmax ? t : (x[p] >= 0 ? 1.0 : t) * reciprocal(1.0 + t);
+                if (x[p] == -__builtin_inff()) key[p] = none;
+                sum += __builtin_fmax(key[p], 0.0);
+                __builtin_amdgcn_sched_barrier(0);   // one after the other: side by side they take too many registers
+            }
+            double by = 1.0;
+            if (softmax) {
+                sum = all_reduce<G>(sum, Sum{});
+                z = (float)sum;
+                by = sum > 0.0 ? reciprocal(sum) : 1.0;
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                key[p] = fma(key[p], by, (double)b[p]);   // -inf is `none`, a bias's too
+            }
+        } else {
+            if (softmax && !a.renorm) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) z += x[p] == -__builtin_inff() ? 0.0f : exp_neg(x[p] - m);
+                z = all_reduce<G>(z, Sum{});
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) key[p] = __builtin_fmin((double)x[p], 1e300);   // (sigmoid: +inf)
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            key[p] = bad || key[p] == none ? none : key_of(key[p], p * G + l);
+
+        // ---- groups ----
+        if constexpr (GROUPED) {
+            double *const mykeys = reinterpret_cast<double *>(smem) + (wid * RPW + sub) * EP;
+#pragma unroll
+            for (int p = 0; p < P; ++p) mykeys[p * G + l] = key[p];
+            wave_sync();
+            double best = none, next = none;
+            if (l < a.groups)
+#pragma unroll 4
+                for (int i = 0, c = l % a.group_size; i < a.group_size; ++i) {
+                    const double v = mykeys[l * a.group_size + c];
+                    next = __builtin_fmax(next, __builtin_fmin(best, v));
+                    best = __builtin_fmax(best, v);
+                    if (++c == a.group_size) c = 0;   // each group from another start: other banks
+                }
+            double total = best == none ? none : without_expert(best);
+            if (a.group_best > 1 && next != none) total += without_expert(next);
+            int better = 0;
+            for (int i = 0; i < a.groups; ++i) {
+                const double o = __shfl(total, first + i);
+                better += o > total || (o == total && i < l);
+            }
+            const unsigned long long kept = __ballot(l < a.groups && better < a.top_groups) >> first;
+            const unsigned magic = ((1u << 20) + a.group_size - 1) / a.group_size;   // e / group_size = e magic >> 20
+#pragma unroll
+            for (int p = 0; p < P; ++p)   // (read again, not held meanwhile)
+                key[p] = (kept >> (((unsigned)(p * G + l) * magic) >> 20)) & 1 ? mykeys[p * G + l] : none;
+            wave_sync();
+        }
+
+        // ---- the k best ----
+        __builtin_amdgcn_sched_barrier(0);
+        sort_keys(key);
+        __builtin_amdgcn_sched_barrier(0);
+        int chosen[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) chosen[c] = -1;
+        const auto choose = [&](auto depth_c) __attribute__((always_inline)) {
+            for (int j = 0; j < a.k; ++j) {
+                const double top = take_best<G, decltype(depth_c)::value>(key, none);
+                const int e = top == none ? -1 : expert_of(top);
+                if (l == j) chosen[0] = e;
+                if constexpr (NC == 2)
+                    if (l + 16 == j) chosen[1] = e;
+            }
+        };
+        if (P > 8 && a.k <= 8)   // shorter lists to move up
+            choose(std::integral_constant<int, 8>{});
+        else
+            choose(std::integral_constant<int, P>{});
+
+        // ---- their weights ----
+        float xs[NC], w[NC];
+        float mc = -__builtin_inff();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const bool there = live && l + c * G < a.k && chosen[c] >= 0;
+            xs[c] = there ? logit(a.x, a.dtype, row + chosen[c]) : -__builtin_inff();
+            mc = fmaxf(mc, xs[c]);
+        }
+        if (a.renorm) mc = all_reduce<G>(mc, Max{});
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const bool there = live && l + c * G < a.k && chosen[c] >= 0;
+            w[c] = there ? chosen_score(a.score, xs[c], a.renorm ? mc : a.score == SCORE_SOFTMAX ? m : 0.0f) : 0.0f;
+            sum += w[c];
+        }
+        if (a.renorm)
+            sum = all_reduce<G>(sum, Sum{});
+        else
+            sum = a.score == SCORE_SOFTMAX ? z : 1.0f;
+        const float by = sum > 0.0f ? a.scale / sum : 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int j = l + c * G;
+            if (live && j < a.k) {
+                const size_t at = (size_t)(t0 + rr) * a.k + j;
+                a.indices[at] = chosen[c];
+                a.weights[at] = bad ? __builtin_nanf("") : w[c] * by;
+                if (a.counts && chosen[c] >= 0) atomicAdd(&count_smem[chosen[c]], 1);
+            }
+        }
+    }
+    if (a.counts) {
+        __syncthreads();
+        int32_t *const counts = a.counts + (size_t)blockIdx.x * count_pitch(a.E);
+        for (int e = tid; e < count_pitch(a.E); e += threads) counts[e] = e < a.E ? count_smem[e] : 0;
+    }
+    if constexpr (FUSE) {
+        if (s.indices) {
+            __syncthreads();   // the chosen experts are in memory
+            sort_block<EP>(s, 0, reinterpret_cast<int(*)[EP]>(smem));
+        }
+    }
+}
+
 // ----------------------------------------------------------------- gradient --
 
 struct RouteGrad {
@@ -452,13 +554,6 @@ struct RouteGrad {
     int score, renorm, dtype;
     float scale;
 };
-
-__device__ __forceinline__ void store_logit(void *x, int dtype, size_t at, float v) {
-    if (dtype == DTYPE_F32)
-        ((float *)x)[at] = v;
-    else
-        ((uint16_t *)x)[at] = (uint16_t)(dtype == DT_BF16 ? pack2<DT_BF16>(v, 0.0f) : pack2<DT_F16>(v, 0.0f));
-}
 
 constexpr int kGradWaves = 4;
 
@@ -501,15 +596,13 @@ route_grad_kernel(RouteGrad a) {
     const bool dense = a.score == SCORE_SOFTMAX && !a.renorm;
     float x[P], m = -__builtin_inff(), z = 0.0f;
     if (dense) {
+        load_logits<G, P>(a.x, a.dtype, row, l, a.E, x);
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            x[p] = live && p * G + l < a.E ? logit(a.x, a.dtype, row + p * G + l) : -__builtin_inff();
-            m = fmaxf(m, x[p]);
-        }
+        for (int p = 0; p < P; ++p) m = fmaxf(m, x[p]);
         m = all_reduce<G>(m, Max{});
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            x[p] = x[p] == -__builtin_inff() ? 0.0f : expf(x[p] - m);
+            x[p] = x[p] == -__builtin_inff() ? 0.0f : exp_neg(x[p] - m);
             z += x[p];
         }
         z = all_reduce<G>(z, Sum{});
@@ -537,18 +630,35 @@ route_grad_kernel(RouteGrad a) {
         if (e[c] < 0) continue;
         float v = g[c];
         if (!dense) v = q[c] * (v - d);
-        if (a.score == SCORE_SIGMOID) v *= 1.0f / (1.0f + expf(xs[c]));
+        if (a.score == SCORE_SIGMOID) v *= chosen_score(SCORE_SIGMOID, -xs[c], 0.0f);   // 1 - s
         atomicAdd(&terms[e[c]], v);   // a repeated expert's terms add up
     }
     wave_sync();
     if (!live) return;
+    float v[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const int at = p * G + l;
-        float v = terms[at];
-        if (dense) v = some ? x[p] * by * (v - d) : 0.0f;
-        if (at < a.E) store_logit(a.dx, a.dtype, row + at, v);
+        v[p] = terms[p * G + l];
+        if (dense) v[p] = some ? x[p] * by * (v[p] - d) : 0.0f;
     }
+    const auto store = [&](auto dtype_c) __attribute__((always_inline)) {
+        constexpr int DT = decltype(dtype_c)::value;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const size_t at = row + p * G + l;
+            if (p * G + l >= a.E) continue;
+            if constexpr (DT == DTYPE_F32)
+                ((float *)a.dx)[at] = v[p];
+            else
+                ((uint16_t *)a.dx)[at] = (uint16_t)pack2<DT>(v[p], 0.0f);
+        }
+    };
+    if (a.dtype == DTYPE_F32)
+        store(std::integral_constant<int, DTYPE_F32>{});
+    else if (a.dtype == DT_BF16)
+        store(std::integral_constant<int, DT_BF16>{});
+    else
+        store(std::integral_constant<int, DT_F16>{});
 }
 
 }  // namespace gbm
