@@ -7,6 +7,8 @@ namespace gbm {
 
 using gbx::Plan;
 
+constexpr gbx::TileCost kBig = {256, 256, 8.0, 1.75, 1.4};
+
 inline Plan plan_f8(int64_t T, int64_t E, int64_t cols, int64_t K, size_t workspace, int cus) {
     const double slices = ceil(K / 128.0);
     Plan best = {false, gbx::TILE_16x64, 1, false};
@@ -23,6 +25,9 @@ inline Plan plan_f8(int64_t T, int64_t E, int64_t cols, int64_t K, size_t worksp
             }
         }
     }
+    // The persistent kernel's stream needs two slices.
+    const double tiles = gbx::row_tiles(T, E, 256) * ceil(cols / 256.0);
+    if (slices >= 2 && ceil(tiles / cus) * (kBig.fix + slices * (2 * tiles > cus ? kBig.slice : kBig.latency)) < least) best = {true, 0, 1, false};
     return best;
 }
 
