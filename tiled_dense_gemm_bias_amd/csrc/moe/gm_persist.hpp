@@ -58,10 +58,13 @@ f8_persist_kernel(Group g) {
     constexpr int BM = 256, BN = 256, NW = 8, WTM = 64, WTN = 128, FM = 4, FN = 8, LAG = 3, NMF = FM * FN;
     constexpr int TILE = 32768, SCALES = 2 * TILE, STAGE = SCALES + 1024 + NW * 256;   // A, W, A's scales, a W scale a lane
     constexpr int STG = 16 * 64 * 2;   // epilogue: 16 rows x 64 columns a wave
+    constexpr bool BIASED = EPI == gbx::EPI_ACT;
     constexpr int NTILE_LD = 8;        // loads of 16 bytes a thread and slice
-    static_assert(2 * STAGE + NW * STG <= 160 * 1024, "LDS");
+    static_assert(2 * STAGE + NW * STG + (BIASED ? 2 * NW * 256 : 16) <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
     __shared__ __attribute__((aligned(1024))) char stage_smem[NW * STG];
+    // The bias of a wave's 128 columns, one slot a wave and tile parity: it comes with the tile's first slice.
+    __shared__ __attribute__((aligned(256))) char bias_smem[BIASED ? 2 * NW * 256 : 16];
 
     // (The lane is formed afresh, lane_now, wherever it is needed: held, with all that follows from it, it would not
     // fit the registers beside the K loop's.)
@@ -159,6 +162,12 @@ f8_persist_kernel(Group g) {
         }
     };
     constexpr int LD = NTILE_LD + 2;
+    auto bias_dma = [&](const Tile &t, int parity) __attribute__((always_inline)) {
+        const int cols = min(N - t.n0 - wn * WTN, WTN);
+        const uint16_t *const b = g.bias + (size_t)t.e * N + t.n0;
+        buffer_load_lds4(make_rsrc(cols > 0 ? b + wn * WTN : b, cols > 0 ? (uint32_t)cols * 2u : 0u), (uint32_t)lane_now() * 4u,
+                         (uint32_t)(uintptr_t)(GBA_LDS void *)bias_smem + (uint32_t)((parity * NW + wid) * 256));
+    };
 
     // ---- fragments ----
     // Row 16 f + tj of the wave's rows: 128 bytes, chunk c at c ^ (tj % 8); chunks tg and tg + 4.
@@ -189,21 +198,25 @@ f8_persist_kernel(Group g) {
     if (!tile_of(0, cur)) return;
     Pos pos = pos_full(cur, true, 0);
     set_off(false);
+    if (BIASED && g.bias) bias_dma(cur, 0);
     static_for<LD>([&](auto i_c) { dma_one(0u, pos, i_c); });
     set_off(tail == 1);
     pos = pos_full(cur, true, 1);
-    static_for<LD>([&](auto i_c) { dma_one((uint32_t)STAGE, pos, i_c); });
-    wait_vmcnt<LD>();
+    static_for<4>([&](auto i_c) { dma_one((uint32_t)STAGE, pos, i_c); });
+    wait_vmcnt<4>();
     block_barrier();
     uint32_t st = 0;   // this slice's stage, in bytes
+    auto read_first = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int f = 0; f < FM; ++f) fa[f] = frag(a_at, f);
+        for (int f = 0; f < FM; ++f) fa[f] = frag(a_at + st, f);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) fw[0][f] = frag(w_at, f);
-    read_scales(0u);
+        for (int f = 0; f < 2; ++f) fw[0][f] = frag(w_at + st, f);
+        read_scales(st);
+    };
+    read_first();
 
     // Product q of a slice: column block q / 4, row blocks in alternating direction.
-    auto fm_of = [](int q) { return (q / FM) & 1 ? FM - 1 - q % FM : q % FM; };
+    auto fm_of = [](int q) { return q % FM; };
     for (int r = 0;; ++r) {
         Tile nxt;
         const bool nxt_live = tile_of(r + 1, nxt);
@@ -230,6 +243,7 @@ f8_persist_kernel(Group g) {
                             const int k2 = here ? kt + 2 : kt + 2 - nk;
                             set_off(k2 == tail);
                             pos = pos_full(here ? cur : nxt, here | nxt_live, k2);
+                            if (BIASED && g.bias && !here && k2 == 0 && nxt_live) bias_dma(nxt, (r + 1) & 1);
                         }
                     }
                 } else {
@@ -238,20 +252,20 @@ f8_persist_kernel(Group g) {
                 }
                 static_for<8>([&](auto q_c) __attribute__((always_inline)) {
                     constexpr int h = decltype(q_c)::value, q = gr * 8 + h, fn = q / FM;
-                    constexpr int fm = (fn & 1) ? FM - 1 - q % FM : q % FM;
+                    constexpr int fm = q % FM;
                     t[q % (LAG + 1)] = gbx::mfma_f8(fw[gr & 1][h / FM], fa[fm]);
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (q >= LAG) {
-                        constexpr int p = q - LAG, pn = p / FM, pm = (pn & 1) ? FM - 1 - p % FM : p % FM;
+                        constexpr int p = q - LAG, pn = p / FM, pm = p % FM;
                         scaled_add<FIRST>(acc[pn][pm], t[p % (LAG + 1)], s[pm]);
                     } else if constexpr (!FIRST) {
-                        constexpr int p = NMF + q - LAG, pn = p / FM, pm = (pn & 1) ? FM - 1 - p % FM : p % FM;
+                        constexpr int p = NMF + q - LAG, pn = p / FM, pm = p % FM;
                         scaled_add<false>(acc[pn][pm], t[p % (LAG + 1)], s_old[pm]);
                     }
+                    // (The loads go on in the next slice, whose other stage this one is.)
+                    if constexpr (gr == 0 && h < 6) dma_one(other, pos, std::integral_constant<int, 4 + h>{});
                     if constexpr (gr == 3) {
-                        dma_one(st, pos, std::integral_constant<int, h>{});
-                        if constexpr (h == 6) dma_one(st, pos, std::integral_constant<int, 8>{});
-                        if constexpr (h == 7) dma_one(st, pos, std::integral_constant<int, 9>{});
+                        if constexpr (h % 2 == 0) dma_one(st, pos, std::integral_constant<int, h / 2>{});
                         if constexpr (h < 2) fw[0][h] = frag(w_at + other, h);
                         if constexpr (h == 2) read_scales(other);
                         if constexpr (h >= 4) fa[fm] = frag(a_at + other, fm);
@@ -292,89 +306,114 @@ f8_persist_kernel(Group g) {
             const int rows_left = cur.rows - cur.m0 - wm * WTM, cols_left = N - cur.n0 - wn * WTN;
             constexpr bool SLOPED = EPI == gbx::EPI_SLOPE && ACT != ACT_NONE;
             constexpr int A = EPI == gbx::EPI_ACT ? ACT : ACT_NONE;
-            const uint16_t *const bias = EPI == gbx::EPI_ACT ? ga->bias : nullptr;
-            // 64 rows of at most 2^24 bytes: offsets below 2^31. Rows of whole 128-byte lines leave non-temporally.
-            const bool lines = N % 64 == 0;
-            auto staged = [&](int f) __attribute__((always_inline)) {
-                return reinterpret_cast<u32x2 *>(stg + ej * 128 + (((2 * f + (eg >> 1)) ^ (ej & 7)) * 16) + (eg & 1) * 8);
-            };
-            auto send = [&](__amdgpu_buffer_rsrc_t out, int fm, int fh) __attribute__((always_inline)) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = fm * 16 + 8 * j + rr, col = fh * 64 + rc * 8;
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(stg + (8 * j + rr) * 128 + ((rc ^ (rr & 7)) * 16));
-                    const uint32_t at = row < rows_left && col < cols_left ? (uint32_t)row * (uint32_t)N * 2u + (uint32_t)col * 2u : kOobOffset;
-                    if (lines)
-                        __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)at, 0, 2 /* nt */);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)at, 0, 0);
-                }
-            };
+            const bool with_z = BIASED && ga->zout != nullptr;
+            const bool has_bias = BIASED && ga->bias != nullptr;
+            // 64 rows of at most 2^24 bytes: offsets below 2^31.
             const __amdgpu_buffer_rsrc_t Cw = make_rsrc((uint16_t *)ga->C + corner, 0x7fffffffu);
-            const bool with_z = EPI == gbx::EPI_ACT && ga->zout != nullptr;
             const __amdgpu_buffer_rsrc_t Pw = make_rsrc(with_z ? ga->zout + corner : nullptr, with_z ? 0x7fffffffu : 0u);
             const __amdgpu_buffer_rsrc_t Zw = make_rsrc(SLOPED ? ga->z + corner : nullptr, SLOPED ? 0x7fffffffu : 0u);
+            const uint32_t pitch = (uint32_t)N * 2u;
+            const uint32_t st_off = (uint32_t)rr * pitch + (uint32_t)rc * 16u, z_off = (uint32_t)ej * pitch + (uint32_t)eg * 8u;
+            char *const put = stg + ej * 128 + (eg & 1) * 8;
+            const char *const get = stg + rr * 128 + ((rc ^ (rr & 7)) * 16);
+            // WHOLE: all 64 x 128 values are there and rows are whole 128-byte lines, which leave non-temporally. (Others
+            // share lines with the tile's next stores, and are left to the L2 to join.)
+            auto store_all = [&](auto whole_c) __attribute__((always_inline)) {
+                constexpr bool WHOLE = decltype(whole_c)::value;
+                constexpr int NG = 2 * FM;
+                // Group n: rows 16 (n % FM) .., columns 64 (n / FM) ..
+                auto send = [&](__amdgpu_buffer_rsrc_t out, const u32x4 (&v)[2], int n) __attribute__((always_inline)) {
 #pragma unroll
-            for (int fh = 0; fh < 2; ++fh) {
-                f32x4 bq[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int col = fh * 64 + 16 * f + 4 * eg;
-                    bq[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    if (bias && col < cols_left) {
-                        const u32x2 b = *reinterpret_cast<const u32x2 *>(bias + (size_t)cur.e * N + cur.n0 + wn * WTN + col);
-                        bq[f] = f32x4{to_f32<ODT>(b.x & 0xffffu), to_f32<ODT>(b.x >> 16), to_f32<ODT>(b.y & 0xffffu), to_f32<ODT>(b.y >> 16)};
+                    for (int j = 0; j < 2; ++j) {
+                        const int row = n % FM * 16 + 8 * j, col = n / FM * 64;
+                        if constexpr (WHOLE) {
+                            __builtin_amdgcn_raw_buffer_store_b128(v[j], out, (int)st_off, (int)((uint32_t)row * pitch) + col * 2, 2 /* nt */);
+                        } else {
+                            const bool there = row + rr < rows_left && col + rc * 8 < cols_left;
+                            __builtin_amdgcn_raw_buffer_store_b128(v[j], out, (int)(there ? st_off + (uint32_t)row * pitch + (uint32_t)col * 2u : kOobOffset), 0, 0);
+                        }
                     }
-                }
-                // z of 16 rows (a lane: one row, four columns a block), one group ahead of its use.
-                u32x2 z[2][4];
-                auto load_z = [&](int fm) __attribute__((always_inline)) {
+                };
+                auto fetch = [&](u32x4 (&v)[2]) __attribute__((always_inline)) {
+                    v[0] = *reinterpret_cast<const u32x4 *>(get);
+                    v[1] = *reinterpret_cast<const u32x4 *>(get + 1024);
+                };
+                u32x2 z[2][4];   // of a group (a lane: one row, four columns a block), a group ahead of its use
+                auto load_z = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
-                        const int row = fm * 16 + ej, col = fh * 64 + 16 * f + 4 * eg;
-                        const uint32_t at = row < rows_left && col < cols_left ? (uint32_t)row * (uint32_t)N * 2u + (uint32_t)col * 2u : kOobOffset;
-                        z[fm & 1][f] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(Zw, (int)at, 0, 0));
+                        const int row = n % FM * 16, col = n / FM * 64 + 16 * f;
+                        const bool there = WHOLE || (row + ej < rows_left && col + 4 * eg < cols_left);
+                        z[n & 1][f] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(Zw, (int)(there ? z_off + (uint32_t)row * pitch + (uint32_t)col * 2u : kOobOffset), 0, 0));
                     }
                 };
                 if constexpr (SLOPED) load_z(0);
+                f32x4 bq[BIASED ? 4 : 1];
+                u32x4 v[2];
 #pragma unroll
-                for (int fm = 0; fm < FM; ++fm) {
-                    if constexpr (SLOPED)
-                        if (fm + 1 < FM) load_z(fm + 1);
-                    f32x4 v[4];
+                for (int n = 0; n <= NG; ++n) {
+                    if (n > 0) fetch(v);   // (a wave's LDS instructions run in order)
+                    if (n < NG) {
+                        const int fm = n % FM, fh = n / FM;
+                        if constexpr (SLOPED)
+                            if (n + 1 < NG) load_z(n + 1);
+                        if constexpr (BIASED) {
+                            if (fm == 0) {
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const float(&s4)[4] = acc[4 * fh + f][fm];
-                        v[f] = f32x4{s4[0], s4[1], s4[2], s4[3]} + bq[f];
-                    }
-                    if (with_z) {
-#pragma unroll
-                        for (int f = 0; f < 4; ++f) *staged(f) = u32x2{pack2<ODT>(v[f][0], v[f][1]), pack2<ODT>(v[f][2], v[f][3])};
-                        wave_sync();
-                        send(Pw, fm, fh);
-                        wave_sync();
-                    }
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        if constexpr (SLOPED) {
-                            const u32x2 q = z[fm & 1][f];
-                            v[f][0] *= gbx::act_slope<ACT>(to_f32<ODT>(q.x & 0xffffu));
-                            v[f][1] *= gbx::act_slope<ACT>(to_f32<ODT>(q.x >> 16));
-                            v[f][2] *= gbx::act_slope<ACT>(to_f32<ODT>(q.y & 0xffffu));
-                            v[f][3] *= gbx::act_slope<ACT>(to_f32<ODT>(q.y >> 16));
+                                for (int f = 0; f < 4; ++f) {
+                                    bq[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+                                    if (has_bias) {
+                                        const u32x2 b = *reinterpret_cast<const u32x2 *>(bias_smem + ((r & 1) * NW + wid) * 256 + fh * 128 + f * 32 + eg * 8);
+                                        bq[f] = f32x4{to_f32<ODT>(b.x & 0xffffu), to_f32<ODT>(b.x >> 16), to_f32<ODT>(b.y & 0xffffu), to_f32<ODT>(b.y >> 16)};
+                                    }
+                                }
+                            }
                         }
-                        *staged(f) = u32x2{pack2<ODT>(act_fn<A>(v[f][0]), act_fn<A>(v[f][1])), pack2<ODT>(act_fn<A>(v[f][2]), act_fn<A>(v[f][3]))};
+                        f32x4 s4[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const float(&q)[4] = acc[4 * fh + f][fm];
+                            s4[f] = f32x4{q[0], q[1], q[2], q[3]};
+                            if constexpr (BIASED) s4[f] += bq[f];
+                        }
+                        auto staged = [&](int f) __attribute__((always_inline)) {
+                            return reinterpret_cast<u32x2 *>(put + (((2 * f + (eg >> 1)) ^ (ej & 7)) * 16));
+                        };
+                        if (BIASED && with_z) {
+                            u32x4 p[2];
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) *staged(f) = u32x2{pack2<ODT>(s4[f][0], s4[f][1]), pack2<ODT>(s4[f][2], s4[f][3])};
+                            wave_sync();
+                            fetch(p);
+                            send(Pw, p, n);
+                        }
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            f32x4 a = s4[f];
+                            if constexpr (SLOPED) {
+                                const u32x2 q = z[n & 1][f];
+                                a[0] *= gbx::act_slope<ACT>(to_f32<ODT>(q.x & 0xffffu));
+                                a[1] *= gbx::act_slope<ACT>(to_f32<ODT>(q.x >> 16));
+                                a[2] *= gbx::act_slope<ACT>(to_f32<ODT>(q.y & 0xffffu));
+                                a[3] *= gbx::act_slope<ACT>(to_f32<ODT>(q.y >> 16));
+                            }
+                            *staged(f) = u32x2{pack2<ODT>(act_fn<A>(a[0]), act_fn<A>(a[1])), pack2<ODT>(act_fn<A>(a[2]), act_fn<A>(a[3]))};
+                        }
+                        wave_sync();
                     }
-                    wave_sync();
-                    send(Cw, fm, fh);
-                    wave_sync();
+                    if (n > 0) send(Cw, v, n - 1);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            }
+            };
+            if (rows_left >= WTM && cols_left >= WTN && N % 64 == 0)
+                store_all(std::true_type{});
+            else
+                store_all(std::false_type{});
         }
         __builtin_amdgcn_sched_barrier(0);
         if (!nxt_live) break;
         cur = nxt;
+        read_first();   // (again: held across the epilogue, the fragments would take its registers)
     }
     wait_vmcnt<0>();   // no direct-to-LDS write may outlive the workgroup's LDS
 }
