@@ -182,11 +182,11 @@ int f8_product(const void *a_codes, const float *a_scales, const int32_t *offset
     int cus;
     if ((s = hip_result(gba::current_cus(&cus)))) return s;
     const gbm::Plan p = gbm::plan_f8(T, E, N, K, workspace ? workspace_bytes : 0, cus);
-    if (p.big) {
+    if (p.kind == gbm::F8_STREAM) return hip_result((slope ? gbm::f8_stream_slope : gbm::f8_stream_act)[dtype](g, t_stream));
+    if (p.kind == gbm::F8_PERSISTENT) {
         const gbx::LaunchFn *const big[2][2] = {{gbm::big_f8_act_f16, gbm::big_f8_act_bf16}, {gbm::big_f8_slope_f16, gbm::big_f8_slope_bf16}};
         return hip_result(big[slope][dtype][act](g, t_stream));
     }
-    if (p.stream) g.flags |= gbx::GF_STREAM;
     if (p.splits == 1) return hip_result((slope ? gbm::f8_slope : gbm::f8_act)[dtype][p.tile](g, t_stream));
     g.splits = p.splits;
     g.part = (float *)workspace;
