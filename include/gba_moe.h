@@ -160,6 +160,19 @@ int grouped_gemm_act_grad_fp8_block(const void *dc_codes, const float *dc_scales
                                     const float *w_scales, const void *z, void *dA, int64_t T, int64_t E, int64_t N, int64_t K,
                                     int act, int dtype, void *workspace, size_t workspace_bytes);
 
+/* ---------------------------------------------------------- choice of kernel -- */
+
+enum { GBM_RING = 0, GBM_PERSISTENT = 1, GBM_STREAM = 2 };
+typedef struct {
+    int32_t kind;             /* GBM_RING: tiles staged in LDS; GBM_PERSISTENT; GBM_STREAM: few rows, weights read once */
+    int32_t tile_m, tile_n;   /* output tile of a workgroup */
+    int32_t splits;           /* parts that K is split in (GBM_RING) */
+} gbm_plan;
+
+/* What a product in 8 bits of these sizes (T rows in all, K deep) takes on a device of `cus` compute units. Needs no
+ * device. GBA_ERR_SHAPE and GBA_ERR_ALIGN as the products; T, N and K at least 1. */
+int gbm_get_plan(int64_t T, int64_t E, int64_t N, int64_t K, size_t workspace_bytes, int cus, gbm_plan *plan);
+
 #ifdef __cplusplus
 }
 #endif

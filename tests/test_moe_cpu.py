@@ -82,7 +82,7 @@ PRODUCTS = [fwd, dense, dgrad, dense_dgrad]
 def test_exports_and_version(lib):
     src = re.sub(r"/\*.*?\*/", "", open(moe.MOE_HEADER).read(), flags=re.S)
     names = re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(\w+)\s*\(", src, flags=re.M)
-    assert len(names) == 18 and "moe_sort_workspace" in names
+    assert len(names) == 19 and "moe_sort_workspace" in names
     cdll = ctypes.CDLL(moe.MOE_LIB_PATH)
     assert not [n for n in names if not hasattr(cdll, n)]
     assert moe.moe_version().count(".") == 2

@@ -141,13 +141,18 @@ hipError_t launch_route(const gbm::Route &a, const gbm::Sort &s, int64_t blocks)
 
 // ------------------------------------------------------------------- products --
 
+int check_product(int64_t T, int64_t E, int64_t N, int64_t K) {
+    if (T < 0 || N < 0 || K < 0 || E < 1 || E > GBM_MAX_GROUPS || T > kMaxRows || N > kMaxWidth || K > kMaxDepth) return GBA_ERR_SHAPE;
+    return (K % 16) || (N % 8) ? GBA_ERR_ALIGN : GBA_OK;
+}
+
 int f8_product(const void *a_codes, const float *a_scales, const int32_t *offsets, bool grouped, const void *w_codes,
                const float *w_scales, const void *bias, const void *z, void *C, void *preact, int64_t T, int64_t E, int64_t N, int64_t K,
                int act, int dtype, bool slope, void *workspace, size_t workspace_bytes) {
     if (!is16(dtype)) return GBA_ERR_DTYPE;
     if (act < GBA_ACT_NONE || act > GBA_ACT_GELU_TANH) return GBA_ERR_ACT;
-    if (T < 0 || N < 0 || K < 0 || E < 1 || E > GBM_MAX_GROUPS || T > kMaxRows || N > kMaxWidth || K > kMaxDepth) return GBA_ERR_SHAPE;
-    if ((K % 16) || (N % 8)) return GBA_ERR_ALIGN;
+    int s = check_product(T, E, N, K);
+    if (s) return s;
     const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
     const Span spans[] = {{a_codes, size3(T, K, 1), true, false, 16},
                           {a_scales, size3(T, kb, 4), true, false, 4},
@@ -159,8 +164,7 @@ int f8_product(const void *a_codes, const float *a_scales, const int32_t *offset
                           {C, size3(T, N, 2), true, true, 16},
                           {preact, size3(T, N, 2), false, true, 16},
                           {workspace, workspace_bytes, false, true, 16}};
-    int s = check_spans(spans);
-    if (s) return s;
+    if ((s = check_spans(spans))) return s;
     if (T == 0 || N == 0) return GBA_OK;
     if ((s = check_device())) return s;
     gbx::Group g = {};
@@ -182,8 +186,8 @@ int f8_product(const void *a_codes, const float *a_scales, const int32_t *offset
     int cus;
     if ((s = hip_result(gba::current_cus(&cus)))) return s;
     const gbm::Plan p = gbm::plan_f8(T, E, N, K, workspace ? workspace_bytes : 0, cus);
-    if (p.kind == gbm::F8_STREAM) return hip_result((slope ? gbm::f8_stream_slope : gbm::f8_stream_act)[dtype](g, t_stream));
-    if (p.kind == gbm::F8_PERSISTENT) {
+    if (p.kind == GBM_STREAM) return hip_result((slope ? gbm::f8_stream_slope : gbm::f8_stream_act)[dtype](g, t_stream));
+    if (p.kind == GBM_PERSISTENT) {
         const gbx::LaunchFn *const big[2][2] = {{gbm::big_f8_act_f16, gbm::big_f8_act_bf16}, {gbm::big_f8_slope_f16, gbm::big_f8_slope_bf16}};
         return hip_result(big[slope][dtype][act](g, t_stream));
     }
@@ -501,6 +505,17 @@ int grouped_gemm_act_grad_fp8_block(const void *dc_codes, const float *dc_scales
                                     int dtype, void *workspace, size_t workspace_bytes) {
     return f8_product(dc_codes, dc_scales, offsets, true, w_codes, w_scales, nullptr, z, dA, nullptr, T, E, N, K, act, dtype, true,
                       workspace, workspace_bytes);
+}
+
+int gbm_get_plan(int64_t T, int64_t E, int64_t N, int64_t K, size_t workspace_bytes, int cus, gbm_plan *plan) {
+    if (!plan) return GBA_ERR_NULL;
+    const int s = check_product(T, E, N, K);
+    if (s) return s;
+    if (T < 1 || N < 1 || K < 1 || cus < 1) return GBA_ERR_SHAPE;
+    const gbm::Plan p = gbm::plan_f8(T, E, N, K, workspace_bytes, cus);
+    const gbx::TileCost &t = p.kind == GBM_PERSISTENT ? gbm::kBig : p.kind == GBM_STREAM ? gbm::kStream : gbm::kRowTiles[p.tile];
+    *plan = {p.kind, (int32_t)t.bm, (int32_t)t.bn, p.splits};
+    return GBA_OK;
 }
 
 }  // extern "C"

@@ -2,13 +2,13 @@
 #pragma once
 
 #include "../experts/gx_plan.hpp"
+#include "gba_moe.h"
 #include "gm_launch.hpp"
 
 namespace gbm {
 
-enum { F8_RING = 0, F8_PERSISTENT = 1, F8_STREAM = 2 };
 struct Plan {
-    int kind;     // F8_*
+    int kind;     // GBM_RING, ...
     int tile;     // ring kernel: its tile
     int splits;
 };
@@ -25,7 +25,7 @@ constexpr double kSecondPass = 2.3;                             // a launch behi
 
 inline Plan plan_f8(int64_t T, int64_t E, int64_t cols, int64_t K, size_t workspace, int cus) {
     const double slices = ceil(K / 128.0), some = E < T ? E : T;
-    Plan best = {F8_RING, gbx::TILE_16x64, 1};
+    Plan best = {GBM_RING, gbx::TILE_16x64, 1};
     double least = 1e300;
     auto consider = [&](double cost, const Plan &p) {
         if (cost < least) {
@@ -42,17 +42,17 @@ inline Plan plan_f8(int64_t T, int64_t E, int64_t cols, int64_t K, size_t worksp
         for (int s : gbx::kSplits) {
             if (s > 1 && (2 * s > slices || (double)s * T * cols * 4.0 > (double)workspace)) break;
             consider(few * (gbx::ring_cost(t, tiles * s, ceil(slices / s), cus) + (s > 1 ? kSecondPass + 2.0 * s * T * cols * 4.0 / 4.0e6 : 0)),
-                     {F8_RING, i, s});
+                     {GBM_RING, i, s});
         }
     }
     // The persistent kernel's stream needs two slices.
     const double tiles = gbx::row_tiles(T, E, 256) * ceil(cols / 256.0);
     if (slices >= 2)
-        consider(ceil(tiles / cus) * (kBig.fix + slices * (2 * tiles > cus ? kBig.slice : kBig.latency)), {F8_PERSISTENT, 0, 1});
+        consider(ceil(tiles / cus) * (kBig.fix + slices * (2 * tiles > cus ? kBig.slice : kBig.latency)), {GBM_PERSISTENT, 0, 1});
     // Few rows an expert: each workgroup reads them again.
     if (T <= 8 * some) {
         const double n = gbx::row_tiles(T, E, 16) * ceil(cols / 16.0) / cus;
-        consider(1.2 + fmax(n * (kStream.fix + slices * kStream.slice), 2 + slices * kStream.latency), {F8_STREAM, 0, 1});
+        consider(1.2 + fmax(n * (kStream.fix + slices * kStream.slice), 2 + slices * kStream.latency), {GBM_STREAM, 0, 1});
     }
     return best;
 }

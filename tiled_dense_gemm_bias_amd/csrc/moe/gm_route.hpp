@@ -371,7 +371,8 @@ route_kernel(Route a, Sort s) {
     __shared__ __attribute__((aligned(16))) char smem[KEYS > PLACES ? KEYS : PLACES];
     __shared__ int count_smem[EP];
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sub = lane / G;
-    const int l = lane & (G - 1), first = lane - l;
+    int l = lane & (G - 1);
+    const int first = lane - l;
     const double none = -__builtin_inf();
     const long long t0 = (long long)linear_block() * a.tokens;
     const int mine = (int)min((long long)a.tokens, a.T - t0);
@@ -384,6 +385,7 @@ route_kernel(Route a, Sort s) {
         const int rr = pass + wid * RPW + sub;
         const bool live = rr < mine;
         const size_t row = (size_t)(t0 + (live ? rr : 0)) * a.E;
+        asm volatile("" : "+v"(l));   // else the biases and the experts' groups stay in registers from pass to pass, and these run out
         float x[P];
         load_logits<G, P>(a.x, a.dtype, row, l, a.E, x);
         const bool softmax = a.score == SCORE_SOFTMAX;

@@ -33,6 +33,10 @@ POW2_SCALES = 1
 _LIB = None
 
 
+class _Plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kind", "tile_m", "tile_n", "splits")]
+
+
 def _lib():
     global _LIB
     if _LIB is None:
@@ -57,6 +61,7 @@ def _lib():
             "gemm_act_grad_fp8_block": [p] * 6 + [i64] * 3 + [ci, ci, p, sz],
             "grouped_gemm_act_grad_fp8_block": [p] * 7 + [i64] * 4 + [ci, ci, p, sz],
             "gbm_set_stream": [p],
+            "gbm_get_plan": [i64] * 4 + [sz, ci, ctypes.POINTER(_Plan)],
             "gbm_last_hip_error": [],
             "gbm_version": [],
         }
@@ -402,3 +407,16 @@ def grouped_gemm_act_grad_fp8_block(dc_codes, dc_scales, offsets, w_codes, w_sca
     _call("grouped_gemm_act_grad_fp8_block", d, dc_codes.data_ptr(), dc_scales.data_ptr(), offsets.data_ptr(), w_codes.data_ptr(),
           w_scales.data_ptr(), _addr(z), da.data_ptr(), T, E, N, K, _act(act), dt, ws, nb)
     return da
+
+
+_KINDS = ("ring", "persistent", "stream")
+
+
+def plan(T: int, E: int, N: int, K: int, workspace: int = 0, cus: int = 256) -> dict:
+    """Kernel ("ring", "persistent" or "stream"), tile and splits of a product in 8 bits of T rows, E experts of [N,K],
+    with `workspace` bytes on a device of `cus` compute units."""
+    p = _Plan()
+    st = _lib().gbm_get_plan(T, E, N, K, workspace, cus, ctypes.byref(p))
+    if st != 0:
+        raise GbaError(st, "gbm_get_plan")
+    return {"kind": _KINDS[p.kind], "tile_m": p.tile_m, "tile_n": p.tile_n, "splits": p.splits}
