@@ -189,16 +189,18 @@ quantize_weights_kernel(QuantWeights a) {
     const int nb = ceil_div(a.N, 128), kb = ceil_div(a.K, 128);
     const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
     if (block >= (long long)a.E * nb * kb) return;
-    const int k = (int)(block % kb), n = (int)(block / kb % nb), e = (int)(block / kb / nb);
+    const int number = (int)block, k = number % kb, n = number / kb % nb, e = number / kb / nb;
     const int col = k * 128 + (tid & 15) * 8;
     u32x4 v[8];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        // (The first value in the place of one outside: with a branch for each load the compiler made one array of 32
+        // registers of these, copied for each, and 234 registers in all: twice the time.)
         const int row = n * 128 + i * 16 + (tid >> 4);
-        v[i] = u32x4{0u, 0u, 0u, 0u};
-        if (row < a.N && col < a.K)
-            v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.w + ((size_t)e * a.N + row) * a.K + col));
+        const bool there = row < a.N && col < a.K;
+        const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.w + (there ? ((size_t)e * a.N + row) * a.K + col : 0)));
+        v[i] = there ? x : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, top_bits(v[i]));
@@ -226,20 +228,26 @@ quantize_weights_kernel(QuantWeights a) {
     }
     if (!a.codes_t) return;
     __syncthreads();
-    // Thread: 16 codes along N of 4 columns of K.
+    // Thread: 16 codes along N of 4 columns of K, whose words of 4 x 4 codes turn in registers.
+    const int r0 = (tid & 7) * 16, q0 = tid >> 3;
+    u32x4 o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int c = i * 32 + (tid >> 3), r0 = (tid & 7) * 16;
-        u32x4 o;
+        uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w = 0;
+        for (int j = 0; j < 4; ++j) w[j] = reinterpret_cast<const uint32_t *>(tile)[(r0 + 4 * i + j) * 33 + q0];
+        const uint32_t a0 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), a1 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+        const uint32_t b0 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), b1 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+        o[0][i] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);
+        o[1][i] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+        o[2][i] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
+        o[3][i] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+    }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) w |= (uint32_t)tile[(r0 + 4 * q + b) * 132 + c] << (8 * b);
-            o[q] = w;
-        }
-        if (k * 128 + c < a.K && n * 128 + r0 < a.N)   // N is a multiple of 16
-            *reinterpret_cast<u32x4 *>(a.codes_t + ((size_t)e * a.K + k * 128 + c) * a.N + n * 128 + r0) = o;
+    for (int i = 0; i < 4; ++i) {
+        const int c = k * 128 + 4 * q0 + i;
+        if (c < a.K && n * 128 + r0 < a.N)   // N is a multiple of 16
+            *reinterpret_cast<u32x4 *>(a.codes_t + ((size_t)e * a.K + c) * a.N + n * 128 + r0) = o[i];
     }
 }
 
@@ -250,7 +258,7 @@ dequantize_weights_kernel(const uint8_t *__restrict__ codes, const float *__rest
     const int nb = ceil_div(N, 128), kb = ceil_div(K, 128), tid = threadIdx.x;
     const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
     if (block >= (long long)E * nb * kb) return;
-    const int k = (int)(block % kb), n = (int)(block / kb % nb), e = (int)(block / kb / nb);
+    const int number = (int)block, k = number % kb, n = number / kb % nb, e = number / kb / nb;
     const int col = k * 128 + (tid & 15) * 8;
     const float s = scales[((size_t)e * nb + n) * kb + k];
     u32x2 c[8];
