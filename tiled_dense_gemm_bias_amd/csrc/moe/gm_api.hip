@@ -419,7 +419,7 @@ int fp8_quantize(const void *X, const int32_t *rows, void *codes, float *scales,
     if ((s = check_device())) return s;
     gbm::QuantRows a = {(const uint16_t *)X, rows, (uint8_t *)codes, scales, (int)T, (int)K, (int)k, (int)R, (flags & GBM_POW2_SCALES) != 0};
     auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::quantize_rows_kernel<0> : gbm::quantize_rows_kernel<1>;
-    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)T, (int)K), dim3(256), t_stream, a));
+    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)T, (int)K, gbm::kQuantRows), dim3(256), t_stream, a));
 }
 
 int fp8_dequantize(const void *codes, const float *scales, void *X, int64_t R, int64_t K, int dtype) {
@@ -434,7 +434,7 @@ int fp8_dequantize(const void *codes, const float *scales, void *X, int64_t R, i
     if (R == 0 || K == 0) return GBA_OK;
     if ((s = check_device())) return s;
     auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::dequantize_rows_kernel<0> : gbm::dequantize_rows_kernel<1>;
-    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)R, (int)K), dim3(256), t_stream, (const uint8_t *)codes, scales,
+    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)R, (int)K, gbm::kDequantRows), dim3(256), t_stream, (const uint8_t *)codes, scales,
                                   (uint16_t *)X, (int)R, (int)K));
 }
 

@@ -85,6 +85,12 @@ __device__ __forceinline__ uint32_t top_bits(const u32x4 &x) {
     return top;
 }
 
+// The value of the lane N places on among its 16.
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xf, 0xf, true);
+}
+
 struct QuantRows {
     const uint16_t *x;        // [T][K]
     const int32_t *rows;      // [T][k], or null: row t goes to row t
@@ -94,53 +100,44 @@ struct QuantRows {
     int pow2;
 };
 
-// A wave takes 4 rows x 4 blocks, 16 lanes of 8 values a block, whose loads all go out before the first is
-// used; its workgroup 16 rows, whose scales of a block lie side by side.
-constexpr int kQuantRows = 16, kQuantBlocks = 4;
+constexpr int kQuantBlocks = 4;                   // of a row, by one wave: 16 lanes of 8 values a block
+constexpr int kQuantRows = 4, kDequantRows = 16;   // of a workgroup
 
+// A wave takes one row's four blocks: 512 bytes of codes leave together, and the loads of its rows' numbers (a lane each) go
+// out with those of the values. 8192 rows of 4096 bf16 to four rows each take 44 us (4.7 TB/s); two rows a wave 47, four 49,
+// and four with a row in each 16 lanes, in 128-byte pieces, 50 (8 rows of 2048: 2.7, 2.8, 3.5 and 3.9 us).
 template <int DT>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(QuantRows a) {
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    const long long t = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kQuantRows + wid * 4 + (lane >> 4);
-    if (t >= a.T) return;   // whole 16-lane groups
-    const int block0 = blockIdx.y * kQuantBlocks, c0 = block0 * 128 + (lane & 15) * 8;
-    u32x4 v[kQuantBlocks];
-#pragma unroll
-    for (int p = 0; p < kQuantBlocks; ++p) {
-        const int c = c0 + p * 128;
-        v[p] = u32x4{0u, 0u, 0u, 0u};
-        if (c < a.K) v[p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.K + c));
-    }
-    float scale[kQuantBlocks];
-    u32x2 code[kQuantBlocks];
-#pragma unroll
-    for (int p = 0; p < kQuantBlocks; ++p) {
-        uint32_t top = top_bits(v[p]);
-#pragma unroll
-        for (int s = 1; s < 16; s *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, s));
-        float by;
-        block_scale(to_f32<DT>(top), a.pow2 != 0, scale[p], by);
-        code[p] = to_f8<DT>(v[p], by);
-    }
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const long long t = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kQuantRows + wid;
+    const int block = blockIdx.y * kQuantBlocks + (lane >> 4), c = block * 128 + (lane & 15) * 8;
+    if (t >= a.T) return;   // a whole wave
+    const int rows = a.rows ? a.rows[(size_t)t * a.k + min(lane, a.k - 1)] : (int)t;   // of slot `lane` (k <= 32)
+    u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.K + min(c, a.K - 8)));
+    if (c >= a.K) v = u32x4{0u, 0u, 0u, 0u};
+    uint32_t top = top_bits(v);
+    top = max(top, row_ror<8>(top));
+    top = max(top, row_ror<4>(top));
+    top = max(top, row_ror<2>(top));
+    top = max(top, row_ror<1>(top));
+    float scale, by;
+    block_scale(to_f32<DT>(top), a.pow2 != 0, scale, by);
+    const u32x2 code = to_f8<DT>(v, by);
     for (int j = 0; j < a.k; ++j) {
-        const long long r = a.rows ? (long long)a.rows[(size_t)t * a.k + j] : t;
-        if (r < 0 || r >= a.R) continue;
-#pragma unroll
-        for (int p = 0; p < kQuantBlocks; ++p) {
-            const int c = c0 + p * 128;
-            if (c >= a.K) continue;
-            *reinterpret_cast<u32x2 *>(a.codes + (size_t)r * a.K + c) = code[p];
-            if ((lane & 15) == 0) a.scales[(size_t)(block0 + p) * a.R + r] = scale[p];
-        }
+        const int r = __builtin_amdgcn_readlane(rows, j);
+        if ((unsigned)r >= (unsigned)a.R || c >= a.K) continue;
+        *reinterpret_cast<u32x2 *>(a.codes + (size_t)r * a.K + c) = code;
+        if ((lane & 15) == 0) a.scales[(size_t)block * a.R + r] = scale;
     }
 }
 
+// A wave: four rows of four blocks.
 template <int DT>
 __global__ void __launch_bounds__(256)
 dequantize_rows_kernel(const uint8_t *__restrict__ codes, const float *__restrict__ scales, uint16_t *__restrict__ x, int R, int K) {
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    const long long r = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kQuantRows + wid * 4 + (lane >> 4);
+    const long long r = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kDequantRows + wid * 4 + (lane >> 4);
     if (r >= R) return;
     const int block0 = blockIdx.y * kQuantBlocks, c0 = block0 * 128 + (lane & 15) * 8;
     u32x2 c[kQuantBlocks];
@@ -162,9 +159,9 @@ dequantize_rows_kernel(const uint8_t *__restrict__ codes, const float *__restric
     }
 }
 
-// Grid: groups of 16 rows along x and, beyond 2^20 of them, z; groups of blocks along y.
-inline dim3 quant_grid(int rows, int K) {
-    const int groups = ceil_div(rows, kQuantRows), z = ceil_div(groups, 1 << 20);
+// Grid: groups of `per` rows along x and, beyond 2^20 of them, z; groups of blocks along y.
+inline dim3 quant_grid(int rows, int K, int per) {
+    const int groups = ceil_div(rows, per), z = ceil_div(groups, 1 << 20);
     return dim3((unsigned)ceil_div(groups, z), (unsigned)ceil_div(ceil_div(K, 128), kQuantBlocks), (unsigned)z);
 }
 
