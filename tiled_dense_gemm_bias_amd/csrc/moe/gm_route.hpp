@@ -16,7 +16,10 @@
 // The weights are computed from the chosen logits in 32 bits, renormalised sigmoid weights as
 // ratios that do not underflow together: s_i e^-min(m, 0), m the largest chosen logit.
 //
-// What bounds it: instructions and latency. 16384 rows of 256 fp32 logits, k = 8, are 17 MB (3.3 us at 5.1 TB/s).
+// What bounds it: vector instructions, and the latency of small kernels. 16384 rows of 256 fp32 logits with a
+// bias, k = 8, are 17 MB (3.3 us at 5.1 TB/s) and take 15.2 us: 1470 vector instructions a wave of four rows are 74 % of its
+// time (a quarter each for the exponentials and the k rounds). 999 rows of grouped experts take 10 us, 8 rows of 32 experts with
+// their sorting, all in one workgroup, 4.4 us.
 #pragma once
 
 #include "gm_common.hpp"
@@ -154,6 +157,8 @@ count_kernel(const int32_t *__restrict__ indices, int32_t *__restrict__ counts, 
 // take equal ranges of its slots in order. Slots of one expert in a wave's 64 find each other by ballots on
 // the bits of the expert's number, so that a row's place depends on its slot alone, and on no
 // atomic's order. place: LDS, for up to EP experts.
+// 131072 slots of 256 experts in 256 blocks take 6.2 us, 8000 in 63 blocks 4.7: a few dependent accesses (half as many
+// blocks, with half the counts to read, take as long; experts loaded ahead of the counts 7.3 us).
 template <int EP>
 __device__ __forceinline__ void sort_block(const Sort &a, int b, int (*place)[EP]) {
     __shared__ int before_smem[EP], total_smem[EP], wave_sum[kRouteWaves];
@@ -565,7 +570,7 @@ constexpr int kGradWaves = 4;
 //   sigmoid, renormalised:  dx_i = q_i (1 - s_i) (g_i - D)
 //   sigmoid:                dx_i = g_i s_i (1 - s_i)
 // A row's chosen terms go through LDS to the lanes that hold the experts; reading and writing the logits
-// and their gradient once is what bounds it.
+// and their gradient once is what bounds it (16384 x 256 in fp32 7.7 us, 4.6 TB/s).
 template <int G, int P>
 __global__ void __launch_bounds__(kGradWaves * 64)
 route_grad_kernel(RouteGrad a) {
