@@ -13,7 +13,7 @@ from collections import defaultdict
 import pytest
 
 from tests import test_isa_cpu as isa
-from tests.test_isa_experts_cpu import early_writes, kinds
+from tests.test_isa_experts_cpu import early_writes, kinds, registers
 from tiled_dense_gemm_bias_amd import moe
 
 pytestmark = isa.pytestmark
@@ -99,3 +99,39 @@ def test_operands_of_matrix_instructions_are_written_in_time(kernels):
     meta, code = kernels
     for n in kinds(meta, "f8_persist"):
         assert not early_writes(code[n]), (n, early_writes(code[n])[:3])
+
+
+def early_reads(code):
+    """Vector instructions that read a matrix instruction's sums too soon: fewer than LAG others stand between (each waits
+    for the one before, 32 cycles), and fewer than 18 wait states of instructions and s_nop."""
+    lag, bad, written, states, count = 3, [], {}, 0, 0
+    for t in code:
+        if t[0] == "s_nop":
+            states += int(t[1], 0) + 1
+            continue
+        if t[0].startswith("v_") and not t[0].startswith("v_mfma"):
+            read = t[1:] if t[0].startswith("v_fmac") else t[2:]
+            for x in read:
+                for r in registers(x):
+                    if r in written and count - written[r][0] < lag and states - written[r][1] < 18:
+                        bad.append((" ".join(t), count - written[r][0], states - written[r][1]))
+            for r in registers(t[1]) if len(t) > 1 else ():
+                written.pop(r, None)
+        states += 1
+        if t[0].startswith("v_mfma"):
+            count += 1
+            for r in registers(t[1]):
+                written[r] = (count, states)
+    return bad
+
+
+def test_sums_of_matrix_instructions_are_read_late_enough(kernels):
+    meta, code = kernels
+    product = ["v_mfma_f32_16x16x128_f8f6f4", "v[0:3]", "v[8:15]", "v[16:23]", "0"]
+    other = ["v_mfma_f32_16x16x128_f8f6f4", "v[4:7]", "v[8:15]", "v[16:23]", "0"]
+    add = ["v_fmac_f32_e32", "v30", "v2", "v31"]
+    assert early_reads([product, other, other, add]) and not early_reads([product, other, other, other, add])
+    assert not early_reads([product, ["s_nop", "7"], ["s_nop", "7"], ["s_nop", "7"], add])
+    for n in kinds(meta, "f8_persist"):
+        adds = [t for t in code[n] if t[0].startswith("v_fmac_f32")]
+        assert len(adds) >= 128 and not early_reads(code[n]), (n, len(adds), early_reads(code[n])[:3])
