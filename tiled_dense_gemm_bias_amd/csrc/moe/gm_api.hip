@@ -476,8 +476,9 @@ int fp8_dequantize_weights(const void *codes, const float *scales, void *W, int6
     if (E == 0 || N == 0 || K == 0) return GBA_OK;
     if ((s = check_device())) return s;
     auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::dequantize_weights_kernel<0> : gbm::dequantize_weights_kernel<1>;
-    return hip_result(gbm::launch(kernel, gba::tile_grid(E * nb * kb), dim3(256), t_stream, (const uint8_t *)codes, scales, (uint16_t *)W,
-                                  (int)E, (int)N, (int)K));
+    const int64_t units = E * ((N + gbm::kDequantWeightRows - 1) / gbm::kDequantWeightRows) * ((kb + gbm::kQuantBlocks - 1) / gbm::kQuantBlocks);
+    return hip_result(gbm::launch(kernel, gba::tile_grid(units), dim3(256), t_stream, (const uint8_t *)codes, scales, (uint16_t *)W, (int)E,
+                                  (int)N, (int)K));
 }
 
 int gemm_bias_act_fp8_block(const void *a_codes, const float *a_scales, const void *w_codes, const float *w_scales, const void *bias,

@@ -249,29 +249,29 @@ quantize_weights_kernel(QuantWeights a) {
     }
 }
 
-// x [E][N][K] from codes and scales [E][N blocks][K blocks].
+// x [E][N][K] from codes and scales [E][N blocks][K blocks]. A wave takes eight rows of four blocks of one expert: a row's 1 KiB
+// leave together.
+constexpr int kDequantWeightRows = 32;   // of a workgroup: within one block of 128
+
 template <int DT>
 __global__ void __launch_bounds__(256)
 dequantize_weights_kernel(const uint8_t *__restrict__ codes, const float *__restrict__ scales, uint16_t *__restrict__ x, int E, int N, int K) {
-    const int nb = ceil_div(N, 128), kb = ceil_div(K, 128), tid = threadIdx.x;
-    const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
-    if (block >= (long long)E * nb * kb) return;
-    const int number = (int)block, k = number % kb, n = number / kb % nb, e = number / kb / nb;
-    const int col = k * 128 + (tid & 15) * 8;
-    const float s = scales[((size_t)e * nb + n) * kb + k];
-    u32x2 c[8];
+    constexpr int R = kDequantWeightRows / 4;
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int nb = ceil_div(N, 128), kb = ceil_div(K, 128), parts = ceil_div(N, kDequantWeightRows), wide = ceil_div(kb, kQuantBlocks);
+    const long long unit = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+    if (unit >= (long long)E * parts * wide) return;
+    const int number = (int)unit, n0 = number / wide % parts * kDequantWeightRows + wid * R, e = number / wide / parts;
+    const int k = number % wide * kQuantBlocks + (lane >> 4), col = k * 128 + (lane & 15) * 8;
+    if (col >= K) return;
+    const float s = scales[((size_t)e * nb + n0 / 128) * kb + k];
+    u32x2 c[R];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = n * 128 + i * 16 + (tid >> 4);
-        c[i] = u32x2{0u, 0u};
-        if (row < N && col < K) c[i] = *reinterpret_cast<const u32x2 *>(codes + ((size_t)e * N + row) * K + col);
-    }
+    for (int i = 0; i < R; ++i)   // (the last row in the place of one past it)
+        c[i] = *reinterpret_cast<const u32x2 *>(codes + ((size_t)e * N + min(n0 + i, N - 1)) * K + col);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = n * 128 + i * 16 + (tid >> 4);
-        if (row < N && col < K)
-            __builtin_nontemporal_store(from_f8<DT>(c[i], s), reinterpret_cast<u32x4 *>(x + ((size_t)e * N + row) * K + col));
-    }
+    for (int i = 0; i < R; ++i)
+        if (n0 + i < N) __builtin_nontemporal_store(from_f8<DT>(c[i], s), reinterpret_cast<u32x4 *>(x + ((size_t)e * N + n0 + i) * K + col));
 }
 
 }  // namespace gbm

@@ -17,7 +17,7 @@
 // ratios that do not underflow together: s_i e^-min(m, 0), m the largest chosen logit.
 //
 // What bounds it: vector instructions, and the latency of small kernels. 16384 rows of 256 fp32 logits with a
-// bias, k = 8, are 17 MB (3.3 us at 5.1 TB/s) and take 15.2 us: 1470 vector instructions a wave of four rows are 74 % of its
+// bias, k = 8, are 17 MB (3.3 us at 5.1 TB/s) and take 15 us: 1400 vector instructions a wave of four rows are 71 % of its
 // time (a quarter each for the exponentials and the k rounds). 999 rows of grouped experts take 10 us, 8 rows of 32 experts with
 // their sorting, all in one workgroup, 4.4 us.
 #pragma once
@@ -322,21 +322,28 @@ __device__ __forceinline__ float chosen_score(int score, float x, float m) {
     return (x >= 0 ? 1.0f : m >= 0 ? t : exp_neg(x - m)) / (1.0f + t);
 }
 
+// p r + c with c in scalar registers (left to itself the compiler copies each c to vector registers for an instruction that
+// overwrites it: two more instructions a step).
+__device__ __forceinline__ double fma_to(double p, double r, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(p), "v"(r), "s"(c));
+    return d;
+}
+
 // e^d for d <= 0 in 64 bits, within 2^-46 (the keys keep 42): d = n ln 2 + r, |r| <= ln 2 / 2, and e^r by its series up
 // to r^11 (the next term is 2^-47).
 __device__ __forceinline__ double exp_neg(double d) {
     const double c = __builtin_fmax(d, -800.0);
     const double n = __builtin_rint(c * 1.4426950408889634);
     const double r = fma(n, -1.9082149292705877e-10, fma(n, -6.93147180369123816490e-01, c));
-    double p = 1.0 / 39916800.0;
-    p = fma(p, r, 1.0 / 3628800.0);
-    p = fma(p, r, 1.0 / 362880.0);
-    p = fma(p, r, 1.0 / 40320.0);
-    p = fma(p, r, 1.0 / 5040.0);
-    p = fma(p, r, 1.0 / 720.0);
-    p = fma(p, r, 1.0 / 120.0);
-    p = fma(p, r, 1.0 / 24.0);
-    p = fma(p, r, 1.0 / 6.0);
+    double p = fma(1.0 / 39916800.0, r, 1.0 / 3628800.0);
+    p = fma_to(p, r, 1.0 / 362880.0);
+    p = fma_to(p, r, 1.0 / 40320.0);
+    p = fma_to(p, r, 1.0 / 5040.0);
+    p = fma_to(p, r, 1.0 / 720.0);
+    p = fma_to(p, r, 1.0 / 120.0);
+    p = fma_to(p, r, 1.0 / 24.0);
+    p = fma_to(p, r, 1.0 / 6.0);
     p = fma(p, r, 0.5);
     p = fma(p, r, 1.0);
     p = fma(p, r, 1.0);
