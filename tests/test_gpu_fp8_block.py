@@ -109,7 +109,8 @@ def test_quantise_every_value_on_a_border(dtype, pow2):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("T,k,H,R", [(1, 1, 16, 3), (8, 2, 2048, 16), (5, 8, 4112, 40), (17, 9, 1008, 200), (2, 32, 272, 64)])
+@pytest.mark.parametrize("T,k,H,R", [(1, 1, 16, 3), (8, 2, 2048, 16), (5, 8, 4112, 40), (17, 9, 1008, 200), (2, 32, 272, 64), (33, 5, 128, 200),
+                                     (70, 3, 256, 300), (9, 32, 112, 400), (3, 32, 240, 100)])
 def test_quantise_to_rows(T, k, H, R, dtype):
     say("quantise to rows", T, k, H, R, dtype)
     rows, x, _, _ = move_case(T, k, H, R, dtype)

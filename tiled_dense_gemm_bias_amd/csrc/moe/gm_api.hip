@@ -418,8 +418,11 @@ int fp8_quantize(const void *X, const int32_t *rows, void *codes, float *scales,
     if (T == 0 || K == 0 || R == 0) return GBA_OK;
     if ((s = check_device())) return s;
     gbm::QuantRows a = {(const uint16_t *)X, rows, (uint8_t *)codes, scales, (int)T, (int)K, (int)k, (int)R, (flags & GBM_POW2_SCALES) != 0};
-    auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::quantize_rows_kernel<0> : gbm::quantize_rows_kernel<1>;
-    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)T, (int)K, gbm::kQuantRows), dim3(256), t_stream, a));
+    void (*const kernels[2][3])(gbm::QuantRows) = {{gbm::quantize_rows_kernel<0, 1>, gbm::quantize_rows_kernel<0, 2>, gbm::quantize_rows_kernel<0, 4>},
+                                                   {gbm::quantize_rows_kernel<1, 1>, gbm::quantize_rows_kernel<1, 2>, gbm::quantize_rows_kernel<1, 4>}};
+    const int which = K <= 128 ? 0 : K <= 256 ? 1 : 2, blocks = 1 << which;
+    return hip_result(gbm::launch(kernels[dtype][which], gbm::quant_grid((int)T, (int)K, 4 * gbm::kQuantBlocks / blocks, blocks), dim3(256),
+                                  t_stream, a));
 }
 
 int fp8_dequantize(const void *codes, const float *scales, void *X, int64_t R, int64_t K, int dtype) {
@@ -434,7 +437,7 @@ int fp8_dequantize(const void *codes, const float *scales, void *X, int64_t R, i
     if (R == 0 || K == 0) return GBA_OK;
     if ((s = check_device())) return s;
     auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::dequantize_rows_kernel<0> : gbm::dequantize_rows_kernel<1>;
-    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)R, (int)K, gbm::kDequantRows), dim3(256), t_stream, (const uint8_t *)codes, scales,
+    return hip_result(gbm::launch(kernel, gbm::quant_grid((int)R, (int)K, gbm::kDequantRows, gbm::kQuantBlocks), dim3(256), t_stream, (const uint8_t *)codes, scales,
                                   (uint16_t *)X, (int)R, (int)K));
 }
 

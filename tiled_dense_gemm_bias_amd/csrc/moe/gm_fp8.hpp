@@ -101,20 +101,23 @@ struct QuantRows {
     int pow2;
 };
 
-constexpr int kQuantBlocks = 4;                   // of a row, by one wave: 16 lanes of 8 values a block
-constexpr int kQuantRows = 4, kDequantRows = 16;   // of a workgroup
+constexpr int kQuantBlocks = 4;     // a wave: 16 lanes of 8 values a block
+constexpr int kDequantRows = 16;    // of a workgroup
 
-// A wave takes one row's four blocks: 512 bytes of codes leave together, and the loads of its rows' numbers (a lane each) go
+// B = 4: a wave takes one row's four blocks: 512 bytes of codes leave together, and the loads of its rows' numbers (a lane each) go
 // out with those of the values. 8192 rows of 4096 bf16 to four rows each take 44 us (4.7 TB/s); two rows a wave 47, four 49,
 // and four with a row in each 16 lanes, in 128-byte pieces, 50 (8 rows of 2048: 2.7, 2.8, 3.5 and 3.9 us).
-template <int DT>
+// B = 1, 2: rows of no more blocks than that, 4 / B of them a wave (300000 rows of 128: 63 us with B = 4, 24 with 1; 100000 of 384 27).
+template <int DT, int B>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(QuantRows a) {
+    constexpr int N = kQuantBlocks / B;   // rows a wave
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const long long t = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kQuantRows + wid;
-    const int block = blockIdx.y * kQuantBlocks + (lane >> 4), c = block * 128 + (lane & 15) * 8;
-    if (t >= a.T) return;   // a whole wave
-    const int rows = a.rows ? a.rows[(size_t)t * a.k + min(lane, a.k - 1)] : (int)t;   // of slot `lane` (k <= 32)
+    const long long t = (((long long)blockIdx.z * gridDim.x + blockIdx.x) * 4 + wid) * N + (N == 1 ? 0 : (lane >> 4) / B);
+    const int block = blockIdx.y * B + (lane >> 4) % B, c = block * 128 + (lane & 15) * 8;
+    if (t >= a.T) return;   // whole rows
+    int rows = (int)t;      // N = 1: of slot `lane` (k <= 32); else of slot 0
+    if (a.rows) rows = a.rows[(size_t)t * a.k + (N == 1 ? min(lane, a.k - 1) : 0)];
     u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.K + min(c, a.K - 8)));
     if (c >= a.K) v = u32x4{0u, 0u, 0u, 0u};
     uint32_t top = top_bits(v);
@@ -126,7 +129,13 @@ quantize_rows_kernel(QuantRows a) {
     block_scale(to_f32<DT>(top), a.pow2 != 0, scale, by);
     const u32x2 code = to_f8<DT>(v, by);
     for (int j = 0; j < a.k; ++j) {
-        const int r = __builtin_amdgcn_readlane(rows, j);
+        int r;
+        if constexpr (N == 1) {
+            r = __builtin_amdgcn_readlane(rows, j);
+        } else {
+            r = rows;
+            if (j + 1 < a.k) rows = a.rows[(size_t)t * a.k + j + 1];
+        }
         if ((unsigned)r >= (unsigned)a.R || c >= a.K) continue;
         *reinterpret_cast<u32x2 *>(a.codes + (size_t)r * a.K + c) = code;
         if ((lane & 15) == 0) a.scales[(size_t)block * a.R + r] = scale;
@@ -161,9 +170,9 @@ dequantize_rows_kernel(const uint8_t *__restrict__ codes, const float *__restric
 }
 
 // Grid: groups of `per` rows along x and, beyond 2^20 of them, z; groups of blocks along y.
-inline dim3 quant_grid(int rows, int K, int per) {
+inline dim3 quant_grid(int rows, int K, int per, int blocks) {
     const int groups = ceil_div(rows, per), z = ceil_div(groups, 1 << 20);
-    return dim3((unsigned)ceil_div(groups, z), (unsigned)ceil_div(ceil_div(K, 128), kQuantBlocks), (unsigned)z);
+    return dim3((unsigned)ceil_div(groups, z), (unsigned)ceil_div(ceil_div(K, 128), blocks), (unsigned)z);
 }
 
 // ------------------------------------------------------------------ weights --
