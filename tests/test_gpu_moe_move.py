@@ -12,7 +12,7 @@ torch = pytest.importorskip("torch")
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
 SIZES = [(1, 1, 8, 1), (3, 2, 72, 10), (8, 2, 2048, 16), (5, 8, 4104, 40), (17, 9, 1000, 200), (2, 32, 264, 64), (33, 3, 8192, 99), (4, 2, 8200, 9),
-         (2, 1, 20000, 2), (40000, 1, 16, 40000)]
+         (2, 1, 20000, 2), (40000, 1, 16, 40000), (2050, 3, 2312, 5000), (2048, 9, 520, 15000), (3001, 2, 4088, 5000)]
 
 
 @pytest.fixture(scope="module", autouse=True)

@@ -398,8 +398,10 @@ int moe_combine_grad(const void *dout, const void *y, const int32_t *rows, const
     a.k = (int)k;
     a.H = (int)H;
     a.R = (int)R;
-    auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::combine_grad_kernel<0> : gbm::combine_grad_kernel<1>;
-    return hip_result(gbm::launch(kernel, gbm::move_grid(T, 1), dim3(gbm::kMoveThreads), t_stream, a));
+    const bool one = gbm::one_wave_a_token(T, (int)H);
+    void (*const kernels[2][2])(gbm::Move) = {{gbm::combine_grad_kernel<0, 4>, gbm::combine_grad_kernel<0, 1>},
+                                              {gbm::combine_grad_kernel<1, 4>, gbm::combine_grad_kernel<1, 1>}};
+    return hip_result(gbm::launch(kernels[dtype][one], gbm::move_grid(one ? (T + 3) / 4 : T, 1), dim3(gbm::kMoveThreads), t_stream, a));
 }
 
 int fp8_quantize(const void *X, const int32_t *rows, void *codes, float *scales, int64_t T, int64_t k, int64_t K, int64_t R, int dtype,

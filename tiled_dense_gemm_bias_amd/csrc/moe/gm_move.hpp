@@ -92,24 +92,30 @@ combine_kernel(Move a) {
     __builtin_nontemporal_store(pack8<DT>(sum), reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.H + h));
 }
 
-// Columns that a thread of combine_grad holds of dout at a time.
-constexpr int kGradPieces = 4, kGradColumns = kMoveThreads * 8 * kGradPieces, kMaxSlots = 32;
+constexpr int kGradPieces = 4, kMaxSlots = 32;   // pieces of eight columns that a thread holds of dout at a time
 
-template <int DT>
+// W waves a token, 4 / W tokens a workgroup. Where tokens are many and their rows short of 4096 one wave a token is faster, as
+// all its lanes have columns (4 slots, a wave and four: 65536 x 512 132 and 403 us, 32768 x 1024 110 and 242, 16384 x 2048 114
+// and 150, 8192 x 2816 82 and 88, 8192 x 4096 114 both, 8192 x 7168 200 and 193); few tokens want more waves each (8 slots, 1000 x
+// 2048: 23 and 19). The next slot's row loaded ahead took longer everywhere (16384 x 2048 115; twice the registers).
+inline bool one_wave_a_token(long long T, int H) { return T >= 2048 && H < 4096; }
+
+template <int DT, int W>
 __global__ void __launch_bounds__(kMoveThreads)
 combine_grad_kernel(Move a) {
+    constexpr int THREADS = 64 * W, COLUMNS = THREADS * 8 * kGradPieces;
     __shared__ float dots[kMoveThreads / 64][kMaxSlots];
-    const long long t = move_token();
-    if (t >= a.T) return;   // a whole workgroup
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, tid = threadIdx.x & (THREADS - 1);
+    const long long t = move_token() * (4 / W) + wid / W;
+    if (t >= a.T) return;   // all of a token's waves
     const int32_t *const rows = a.rows + (size_t)t * a.k;
     for (int j = lane; j < kMaxSlots; j += 64) dots[wid][j] = 0.0f;
     wave_sync();
-    for (int h0 = 0; h0 < a.H; h0 += kGradColumns) {
+    for (int h0 = 0; h0 < a.H; h0 += COLUMNS) {
         float d[kGradPieces][8];
 #pragma unroll
         for (int p = 0; p < kGradPieces; ++p) {
-            const int h = h0 + (p * kMoveThreads + threadIdx.x) * 8;
+            const int h = h0 + (p * THREADS + tid) * 8;
             u32x4 v = {0u, 0u, 0u, 0u};
             if (h < a.H) v = *reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.H + h);
             unpack8<DT>(v, d[p]);
@@ -121,14 +127,14 @@ combine_grad_kernel(Move a) {
             u32x4 v[kGradPieces];
 #pragma unroll
             for (int p = 0; p < kGradPieces; ++p) {
-                const int h = h0 + (p * kMoveThreads + threadIdx.x) * 8;
+                const int h = h0 + (p * THREADS + tid) * 8;
                 v[p] = u32x4{0u, 0u, 0u, 0u};
                 if (h < a.H) v[p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.y + (size_t)r * a.H + h));
             }
             float dot = 0.0f;
 #pragma unroll
             for (int p = 0; p < kGradPieces; ++p) {
-                const int h = h0 + (p * kMoveThreads + threadIdx.x) * 8;
+                const int h = h0 + (p * THREADS + tid) * 8;
                 float f[8], o[8];
                 unpack8<DT>(v[p], f);
 #pragma unroll
@@ -143,13 +149,15 @@ combine_grad_kernel(Move a) {
             if (lane == 0) dots[wid][j] += dot;
         }
     }
-    __syncthreads();
-    const int j = threadIdx.x;
-    if (a.dw && j < a.k) {
+    if constexpr (W > 1)
+        __syncthreads();
+    else
+        wave_sync();
+    if (a.dw && tid < a.k) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kMoveThreads / 64; ++w) s += dots[w][j];
-        a.dw[(size_t)t * a.k + j] = s;
+        for (int w = 0; w < W; ++w) s += dots[wid / W * W + w][tid];
+        a.dw[(size_t)t * a.k + tid] = s;
     }
 }
 
