@@ -2,6 +2,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "../experts/gx_reduce.hpp"
@@ -259,9 +260,13 @@ int moe_route(const void *logits, const float *bias, int32_t *indices, float *we
         a.renorm = (flags & GBM_RENORMALIZE) != 0;
         a.dtype = dtype;
         a.scale = scale;
-        // One pass of one block of up to 256 experts: it sorts as well.
-        const bool fused = sort && !counted && E <= 256 && T <= gbm::kRouteWaves * 4;
+        // One block that sorts as well, where its waves are few enough (8 tokens of 256 grouped experts 10 us, by two kernels
+        // 11 to 12; 64 of 128 experts 10, by two kernels 7 to 9).
+        const bool fused = sort && !counted && E <= 256 && (T <= 32 || (E <= 32 && T <= gbm::kRouteWaves * 4));
         a.tokens = fused ? (int)T : counted ? order.per_block / (int)k : kLeastTokens;
+        // Grouped keys fill a CU's LDS for 16 waves, however many work: as many as there are tokens for (16384 x 256 31 us with four).
+        if (groups > top_groups && E > 64 && !fused && !counted)
+            a.tokens = (int)std::min<int64_t>(((T + kMaxBlocks - 1) / kMaxBlocks + kLeastTokens - 1) / kLeastTokens * kLeastTokens, 64);
         gbm::Sort inside = order;
         if (!fused) inside.indices = nullptr;
         const int64_t n = (T + a.tokens - 1) / a.tokens;

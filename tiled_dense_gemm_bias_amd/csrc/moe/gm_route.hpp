@@ -393,8 +393,8 @@ route_kernel(Route a, Sort s) {
         for (int e = tid; e < a.E; e += threads) count_smem[e] = 0;
         __syncthreads();
     }
-    for (int pass = 0; pass < mine; pass += RPB) {
-        const int rr = pass + wid * RPW + sub;
+    for (int row0 = __builtin_amdgcn_readfirstlane(wid) * RPW; row0 < mine; row0 += RPB) {   // the wave's rows
+        const int rr = row0 + sub;
         const bool live = rr < mine;
         const size_t row = (size_t)(t0 + (live ? rr : 0)) * a.E;
         asm volatile("" : "+v"(l));   // else the biases and the experts' groups stay in registers from pass to pass, and these run out
