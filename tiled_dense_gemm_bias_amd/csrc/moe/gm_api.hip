@@ -127,7 +127,7 @@ hipError_t launch_sort(const gbm::Sort &s) {
 
 template <bool GROUPED>
 hipError_t launch_route(const gbm::Route &a, const gbm::Sort &s, int64_t blocks) {
-    const int waves = (a.tokens * (a.E <= 256 ? 16 : 64) + 63) / 64;   // of one pass
+    const int waves = (a.tokens * (a.E <= 256 ? 16 : a.E <= 512 ? 32 : 64) + 63) / 64;   // of one pass
     const dim3 grid = gba::tile_grid(blocks);
     const dim3 block(s.indices || waves > gbm::kRouteWaves ? gbm::kRouteThreads : waves * 64);
     void (*kernel)(gbm::Route, gbm::Sort) = a.E <= 16    ? gbm::route_kernel<16, 1, GROUPED>
@@ -135,7 +135,7 @@ hipError_t launch_route(const gbm::Route &a, const gbm::Sort &s, int64_t blocks)
                                             : a.E <= 64  ? gbm::route_kernel<16, 4, GROUPED>
                                             : a.E <= 128 ? gbm::route_kernel<16, 8, GROUPED>
                                             : a.E <= 256 ? gbm::route_kernel<16, 16, GROUPED>
-                                            : a.E <= 512 ? gbm::route_kernel<64, 8, GROUPED>
+                                            : a.E <= 512 ? gbm::route_kernel<32, 16, GROUPED>
                                                          : gbm::route_kernel<64, 16, GROUPED>;
     return gbm::launch(kernel, grid, block, t_stream, a, s);
 }

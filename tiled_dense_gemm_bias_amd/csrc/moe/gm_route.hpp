@@ -1,7 +1,7 @@
 // Routing to experts: each token's k best of E experts, their weights, and the sorting of the
 // (token, expert) slots by expert.
 //
-// Selection. A row belongs to G lanes (16, or 64 from 257 experts on), lane l holding experts
+// Selection. A row belongs to G lanes (16; 32 from 257 experts on, 64 from 513), lane l holding experts
 // l, l + G, ... Each expert's value is a 64-bit float whose low 10 bits are replaced by
 // the expert's number, so that one maximum finds the best value and its expert, ties going to the
 // lowest number. Without a bias and without sums over groups the value is the logit itself (the
@@ -19,7 +19,8 @@
 // What bounds it: vector instructions, and the latency of small kernels. 16384 rows of 256 fp32 logits with a
 // bias, k = 8, are 17 MB (3.3 us at 5.1 TB/s) and take 15 us: 1400 vector instructions a wave of four rows are 71 % of its
 // time (a quarter each for the exponentials and the k rounds). 999 rows of grouped experts take 10 us, 8 rows of 32 experts with
-// their sorting, all in one workgroup, 4.4 us.
+// their sorting, all in one workgroup, 3.8 us. As many values in a lane as its registers take (16), as the rounds are a wave's
+// and not a value's: 8192 rows of 384 experts take 9.9 us in 32 lanes each and 13.7 in 64 (with a bias 16.0 and 19.2).
 #pragma once
 
 #include "gm_common.hpp"
@@ -74,7 +75,7 @@ __device__ __forceinline__ double without_expert(double key) {
     return __longlong_as_double(__double_as_longlong(key) & ~(long long)kExpertBits);
 }
 
-// f over the 16 lanes of a row, or over the wave; every lane gets the result.
+// f over a row's G lanes; every lane gets the result.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
@@ -86,11 +87,26 @@ __device__ __forceinline__ double dpp(double v) {
     const unsigned hi = (unsigned)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
     return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
 }
-__device__ __forceinline__ float lane_value(float v, int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); }
-__device__ __forceinline__ double lane_value(double v, int l) {
+// The values of this lane and of the one 16 (32) lanes on or back, as a pair.
+template <int D>
+__device__ __forceinline__ void across(uint32_t v, uint32_t &x, uint32_t &y) {
+    const auto s = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false) : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    x = s[0];
+    y = s[1];
+}
+template <int D, class F>
+__device__ __forceinline__ float join(float v, F f) {
+    uint32_t x, y;
+    across<D>(__float_as_uint(v), x, y);
+    return f(__uint_as_float(x), __uint_as_float(y));
+}
+template <int D, class F>
+__device__ __forceinline__ double join(double v, F f) {
     const long long b = __double_as_longlong(v);
-    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)b, l), hi = (unsigned)__builtin_amdgcn_readlane((int)(b >> 32), l);
-    return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+    uint32_t xl, yl, xh, yh;
+    across<D>((uint32_t)b, xl, yl);
+    across<D>((uint32_t)(b >> 32), xh, yh);
+    return f(__longlong_as_double((long long)(((unsigned long long)xh << 32) | xl)), __longlong_as_double((long long)(((unsigned long long)yh << 32) | yl)));
 }
 template <int G, class T, class F>
 __device__ __forceinline__ T all_reduce(T v, F f) {
@@ -98,7 +114,8 @@ __device__ __forceinline__ T all_reduce(T v, F f) {
     v = f(v, dpp<0x124>(v));
     v = f(v, dpp<0x122>(v));
     v = f(v, dpp<0x121>(v));
-    if constexpr (G == 64) v = f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
+    if constexpr (G >= 32) v = join<16>(v, f);
+    if constexpr (G == 64) v = join<32>(v, f);
     return v;
 }
 struct Max {
@@ -113,7 +130,7 @@ struct Sum {
 template <int G>
 __device__ __forceinline__ bool any_of(bool b, int first) {
     const unsigned long long m = __ballot(b);
-    return G == 64 ? m != 0 : ((m >> first) & 0xffff) != 0;
+    return G == 64 ? m != 0 : ((m >> first) & ((1ull << (G & 63)) - 1)) != 0;
 }
 
 // Largest first (Batcher's odd-even merge sort).
