@@ -8,7 +8,7 @@
 // on the right side, or on the border. With powers of two for scales everything is exact.
 //
 // HBM is what bounds all of these (a large copy runs at 5.1 TB/s): 8 weights of 8192 x 4096 in both layouts 172 us (6.2
-// TB/s) and back 145 to 185 each, 32768 rows of 4096 back 65 us (6.2 TB/s).
+// TB/s) and back 134 to 167 each, 32768 rows of 4096 back 65 us (6.2 TB/s).
 #pragma once
 
 #include "gm_common.hpp"
