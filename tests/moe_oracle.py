@@ -50,13 +50,12 @@ def route(x, bias, k, score="softmax", renorm=True, scale=1.0, groups=1, top_gro
     value = x64 if plain else s + (0 if bias is None else bias.double())
     value = torch.where(left, value.clamp(-1e300, 1e300), torch.full_like(value, -math.inf))
     if groups > top_groups:
-        for t in range(T):
-            v = value[t].view(groups, -1).sort(dim=1, descending=True).values[:, :group_best]
-            total = [(sum(float(q) for q in g if q != -math.inf), i) for i, g in enumerate(v) if g[0] != -math.inf]
-            kept = {i for _, i in sorted(total, key=lambda p: (-p[0], p[1]))[:top_groups]}
-            for i in range(groups):
-                if i not in kept:
-                    value[t].view(groups, -1)[i] = -math.inf
+        by = value.view(T, groups, -1)
+        best = by.sort(dim=2, descending=True).values[:, :, :group_best]
+        total = torch.where(best == -math.inf, torch.zeros_like(best), best).sum(2)
+        total = torch.where(best[:, :, 0] == -math.inf, torch.full_like(total, -math.inf), total)
+        kept = torch.zeros_like(total, dtype=torch.bool).scatter(1, total.sort(dim=1, descending=True, stable=True).indices[:, :top_groups], True)
+        value = torch.where(kept[:, :, None], by, torch.full_like(by, -math.inf)).view(T, E)
     v, idx = value.sort(dim=1, descending=True, stable=True)
     v, idx = v[:, :k], idx[:, :k]
     none = (v == -math.inf) | bad[:, None]

@@ -282,3 +282,21 @@ def test_a_repeated_expert_and_numbers_out_of_range():
             legal = torch.where((idx >= 0) & (idx < 20), idx, -1)
             want, size, depth = orc.route_grad(x, legal, dw, score, renorm)
             eo.check("dx", dx, want, eo.with_rounding(want, (2 * depth[:, None] + 60) * 2.0 ** -24 * size + 2.0 ** -120, torch.float32))
+
+
+# Around the sizes where the launches change: one workgroup for routing and sorting, tokens a workgroup, lanes a row.
+BORDERS = [(32, 256, 8, 8, 4), (33, 256, 8, 8, 4), (32, 200, 6, 1, 1), (33, 200, 6, 1, 1), (64, 32, 4, 4, 2), (65, 32, 4, 4, 2), (63, 31, 3, 1, 1),
+           (5, 288, 8, 8, 3), (64, 288, 32, 4, 2), (100, 512, 9, 16, 5), (70, 513, 9, 3, 2), (12300, 72, 3, 8, 3), (13001, 264, 4, 8, 2),
+           (4097, 1024, 2, 16, 4), (20001, 96, 2, 12, 3)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top", BORDERS)
+def test_borders(T, E, k, groups, top, score):
+    say("borders", T, E, k, groups, top, score)
+    x, g = logits(T + 5 * E, T, E, "f32")
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    x[T // 2, E // 3:] = -math.inf
+    x[T - 1] = -math.inf
+    check(x, k, bias, score=score, groups=groups, top_groups=top, group_best=2 if groups > 1 else 1, scale=2.5)
+    check(x.bfloat16(), k, None, score=score, groups=groups, top_groups=top, renormalize=False)
