@@ -37,11 +37,12 @@ class Routing:
         return gba.moe_dispatch(x, self.rows, x.new_empty(self.rows.numel(), x.shape[1]))
 
     def combine(self, y, weighted=True):
-        """Each token's sum over its rows; without weights, what dispatch's gradient is."""
-        return gba.moe_combine(y, self.rows, self.weights if weighted else None, y.new_empty(self.rows.shape[0], y.shape[1]))
+        """Each token's sum over its rows, in fp32; without weights, what dispatch's gradient is."""
+        out = y.new_empty(self.rows.shape[0], y.shape[1], dtype=torch.float32)
+        return gba.moe_combine(y, self.rows, self.weights if weighted else None, out)
 
     def backward(self, dout, y):
-        """(dy, dlogits) of combine(y), for its gradient dout."""
+        """(dy, dlogits) of combine(y), for its gradient dout (fp32)."""
         dy, dweights, dlogits = torch.empty_like(y), torch.empty_like(self.weights), torch.empty_like(self.logits)
         gba.moe_combine_grad(dout, y, self.rows, self.weights, dy, dweights)
         return dy, gba.moe_route_grad(self.logits, self.indices, dweights, dlogits)
@@ -150,8 +151,8 @@ def gradients(layer, router, x, goal, top):
     """(loss: squared error of a token, d router) with the layer's in layer.grads. router [E, width] fp32."""
     to = Routing(x.float() @ router.T, top)
     y, saved = layer.forward(to.dispatch(x), to.offsets)
-    off = to.combine(y).float() - goal.float()
-    dy, dlogits = to.backward((off * (2.0 / x.shape[0])).to(layer.dtype), y)
+    off = to.combine(y) - goal
+    dy, dlogits = to.backward(off * (2.0 / x.shape[0]), y)
     layer.backward(dy, to.offsets, saved)
     return off.square().sum(1).mean(), dlogits.T @ x.float()
 
@@ -178,8 +179,8 @@ def served_errors(layer, router, x, top):
     """Relative errors of the layer's outputs for x in 4 and in 8 bits."""
     to = Routing(x.float() @ router.T, top)
     rows = to.dispatch(x)
-    y, *served = (to.combine(r).float() for r in (layer.forward(rows, to.offsets)[0], Served4Bit(layer).forward(rows, to.offsets),
-                                                  Served8Bit(layer).forward(x, to)))
+    y, *served = (to.combine(r) for r in (layer.forward(rows, to.offsets)[0], Served4Bit(layer).forward(rows, to.offsets),
+                                          Served8Bit(layer).forward(x, to)))
     return [((s - y).norm() / y.norm()).item() for s in served]
 
 

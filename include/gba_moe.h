@@ -93,8 +93,12 @@ size_t moe_sort_workspace(int64_t T, int64_t E, int64_t k);
  * twice holds one of the two. */
 int moe_dispatch(const void *x, const int32_t *rows, void *out, int64_t T, int64_t k, int64_t H, int64_t R, int dtype);
 
-/* out[t] = sum over j of weights[t][j] y[rows[t][j]], in fp32, rounded once: y [R,H], out [T,H]. weights NULL: ones
- * (the gradient of moe_dispatch). A slot of -1 adds weight times 0. */
+/* In the dtype of moe_combine and moe_combine_grad, beside the experts' rows' type: out and dout, the tokens' side,
+ * are fp32, so that a loss is taken from sums that no 16-bit type has rounded, and its gradient is rounded once, in dy. */
+enum { GBM_F32_TOKENS = 256 };
+
+/* out[t] = sum over j of weights[t][j] y[rows[t][j]], in fp32, rounded once (not at all with GBM_F32_TOKENS):
+ * y [R,H], out [T,H]. weights NULL: ones (the gradient of moe_dispatch). A slot of -1 adds weight times 0. */
 int moe_combine(const void *y, const int32_t *rows, const float *weights, void *out, int64_t T, int64_t k, int64_t H,
                 int64_t R, int dtype);
 

@@ -324,6 +324,13 @@ int moe_sort(const int32_t *indices, int32_t *offsets, int32_t *rows, int32_t *s
     return hip_result(launch_sort(order));
 }
 
+// combine's dtype: the experts' rows', and whether the tokens' are in 32 bits.
+static bool split_dtype(int dtype, int *rows, bool *f32) {
+    *rows = dtype & ~GBM_F32_TOKENS;
+    *f32 = (dtype & GBM_F32_TOKENS) != 0;
+    return is16(*rows);
+}
+
 // Tokens, slots, columns and experts' rows of the moves.
 static int check_move(int64_t T, int64_t k, int64_t H, int64_t R) {
     if (T < 0 || k < 1 || k > gbm::kMaxTop || H < 0 || R < 0 || T > kMaxRows / k || R > kMaxRows || H > kMaxWidth) return GBA_ERR_SHAPE;
@@ -341,9 +348,9 @@ int moe_dispatch(const void *x, const int32_t *rows, void *out, int64_t T, int64
     if (T == 0 || H == 0 || R == 0) return GBA_OK;
     if ((s = check_device())) return s;
     gbm::Move a = {};
-    a.x = (const uint16_t *)x;
+    a.x = x;
     a.rows = rows;
-    a.out = (uint16_t *)out;
+    a.out = out;
     a.T = (int)T;
     a.k = (int)k;
     a.H = (int)H;
@@ -354,13 +361,15 @@ int moe_dispatch(const void *x, const int32_t *rows, void *out, int64_t T, int64
 
 int moe_combine(const void *y, const int32_t *rows, const float *weights, void *out, int64_t T, int64_t k, int64_t H, int64_t R,
                 int dtype) {
-    if (!is16(dtype)) return GBA_ERR_DTYPE;
+    int dt;
+    bool f32;
+    if (!split_dtype(dtype, &dt, &f32)) return GBA_ERR_DTYPE;
     int s = check_move(T, k, H, R);
     if (s) return s;
     const Span spans[] = {{y, size3(R, H, 2), true, false, 16},
                           {rows, size3(T, k, 4), H > 0, false, 4},
                           {weights, size3(T, k, 4), false, false, 4},
-                          {out, size3(T, H, 2), true, true, 16}};
+                          {out, size3(T, H, f32 ? 4 : 2), true, true, 16}};
     if ((s = check_spans(spans))) return s;
     if (T == 0 || H == 0) return GBA_OK;
     if ((s = check_device())) return s;
@@ -368,22 +377,25 @@ int moe_combine(const void *y, const int32_t *rows, const float *weights, void *
     a.y = (const uint16_t *)y;
     a.rows = rows;
     a.w = weights;
-    a.out = (uint16_t *)out;
+    a.out = out;
     a.T = (int)T;
     a.k = (int)k;
     a.H = (int)H;
     a.R = (int)R;
     const int pieces = gba::ceil_div((int)H, gbm::kMoveThreads * 8);
-    auto *const kernel = dtype == GBA_DTYPE_F16 ? gbm::combine_kernel<0> : gbm::combine_kernel<1>;
-    return hip_result(gbm::launch(kernel, gbm::move_grid(T, pieces), dim3(gbm::kMoveThreads), t_stream, a));
+    void (*const kernels[2][2])(gbm::Move) = {{gbm::combine_kernel<0, false>, gbm::combine_kernel<0, true>},
+                                              {gbm::combine_kernel<1, false>, gbm::combine_kernel<1, true>}};
+    return hip_result(gbm::launch(kernels[dt][f32], gbm::move_grid(T, pieces), dim3(gbm::kMoveThreads), t_stream, a));
 }
 
 int moe_combine_grad(const void *dout, const void *y, const int32_t *rows, const float *weights, void *dy, float *dweights, int64_t T,
                      int64_t k, int64_t H, int64_t R, int dtype) {
-    if (!is16(dtype)) return GBA_ERR_DTYPE;
+    int dt;
+    bool f32;
+    if (!split_dtype(dtype, &dt, &f32)) return GBA_ERR_DTYPE;
     int s = check_move(T, k, H, R);
     if (s) return s;
-    const Span spans[] = {{dout, size3(T, H, 2), true, false, 16},
+    const Span spans[] = {{dout, size3(T, H, f32 ? 4 : 2), true, false, 16},
                           {y, size3(R, H, 2), true, false, 16},
                           {rows, size3(T, k, 4), true, false, 4},
                           {weights, size3(T, k, 4), false, false, 4},
@@ -393,7 +405,7 @@ int moe_combine_grad(const void *dout, const void *y, const int32_t *rows, const
     if (T == 0 || (!dy && !dweights)) return GBA_OK;
     if ((s = check_device())) return s;
     gbm::Move a = {};
-    a.x = (const uint16_t *)dout;
+    a.x = dout;
     a.y = (const uint16_t *)y;
     a.rows = rows;
     a.w = weights;
@@ -404,9 +416,10 @@ int moe_combine_grad(const void *dout, const void *y, const int32_t *rows, const
     a.H = (int)H;
     a.R = (int)R;
     const bool one = gbm::one_wave_a_token(T, (int)H);
-    void (*const kernels[2][2])(gbm::Move) = {{gbm::combine_grad_kernel<0, 4>, gbm::combine_grad_kernel<0, 1>},
-                                              {gbm::combine_grad_kernel<1, 4>, gbm::combine_grad_kernel<1, 1>}};
-    return hip_result(gbm::launch(kernels[dtype][one], gbm::move_grid(one ? (T + 3) / 4 : T, 1), dim3(gbm::kMoveThreads), t_stream, a));
+    void (*const kernels[2][2][2])(gbm::Move) = {
+        {{gbm::combine_grad_kernel<0, 4, false>, gbm::combine_grad_kernel<0, 4, true>}, {gbm::combine_grad_kernel<0, 1, false>, gbm::combine_grad_kernel<0, 1, true>}},
+        {{gbm::combine_grad_kernel<1, 4, false>, gbm::combine_grad_kernel<1, 4, true>}, {gbm::combine_grad_kernel<1, 1, false>, gbm::combine_grad_kernel<1, 1, true>}}};
+    return hip_result(gbm::launch(kernels[dt][one][f32], gbm::move_grid(one ? (T + 3) / 4 : T, 1), dim3(gbm::kMoveThreads), t_stream, a));
 }
 
 int fp8_quantize(const void *X, const int32_t *rows, void *codes, float *scales, int64_t T, int64_t k, int64_t K, int64_t R, int dtype,

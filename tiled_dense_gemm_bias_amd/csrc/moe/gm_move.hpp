@@ -16,10 +16,12 @@
 namespace gbm {
 
 struct Move {
-    const uint16_t *x, *y;     // tokens' rows [T][H]; experts' rows [R][H]
+    const void *x;             // tokens' rows [T][H] (F32: in 32 bits)
+    const uint16_t *y;         // experts' rows [R][H]
     const int32_t *rows;       // [T][k]
     const float *w;            // [T][k] or null (ones)
-    uint16_t *out, *dy;
+    void *out;                 // as x
+    uint16_t *dy;
     float *dw;                 // [T][k] or null
     int T, k, H, R;
 };
@@ -39,11 +41,11 @@ dispatch_kernel(Move a) {
     const long long t = move_token();
     const int h = (blockIdx.x * kMoveThreads + threadIdx.x) * 8;
     if (t >= a.T || h >= a.H) return;
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.H + h);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>((const uint16_t *)a.x + (size_t)t * a.H + h);
     const int32_t *const rows = a.rows + (size_t)t * a.k;
     for (int j = 0; j < a.k; ++j) {
         const int r = rows[j];
-        if ((unsigned)r < (unsigned)a.R) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(a.out + (size_t)r * a.H + h));
+        if ((unsigned)r < (unsigned)a.R) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>((uint16_t *)a.out + (size_t)r * a.H + h));
     }
 }
 
@@ -60,7 +62,8 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
     return u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
 }
 
-template <int DT>
+// F32: the sums leave as they are, where a caller's own arithmetic on them (a loss, say) is in 32 bits.
+template <int DT, bool F32>
 __global__ void __launch_bounds__(kMoveThreads)
 combine_kernel(Move a) {
     const long long t = move_token();
@@ -89,7 +92,15 @@ combine_kernel(Move a) {
             for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
         }
     }
-    __builtin_nontemporal_store(pack8<DT>(sum), reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.H + h));
+    const size_t at = (size_t)t * a.H + h;
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            __builtin_nontemporal_store(f32x4{sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]},
+                                        reinterpret_cast<f32x4 *>((float *)a.out + at + 4 * i));
+    } else {
+        __builtin_nontemporal_store(pack8<DT>(sum), reinterpret_cast<u32x4 *>((uint16_t *)a.out + at));
+    }
 }
 
 constexpr int kGradPieces = 4, kMaxSlots = 32;   // pieces of eight columns that a thread holds of dout at a time
@@ -100,7 +111,8 @@ constexpr int kGradPieces = 4, kMaxSlots = 32;   // pieces of eight columns that
 // 2048: 23 and 19). The next slot's row loaded ahead took longer everywhere (16384 x 2048 115; twice the registers).
 inline bool one_wave_a_token(long long T, int H) { return T >= 2048 && H < 4096; }
 
-template <int DT, int W>
+// F32: dout as combine's sums, in 32 bits.
+template <int DT, int W, bool F32>
 __global__ void __launch_bounds__(kMoveThreads)
 combine_grad_kernel(Move a) {
     constexpr int THREADS = 64 * W, COLUMNS = THREADS * 8 * kGradPieces;
@@ -116,9 +128,20 @@ combine_grad_kernel(Move a) {
 #pragma unroll
         for (int p = 0; p < kGradPieces; ++p) {
             const int h = h0 + (p * THREADS + tid) * 8;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (h < a.H) v = *reinterpret_cast<const u32x4 *>(a.x + (size_t)t * a.H + h);
-            unpack8<DT>(v, d[p]);
+            const size_t at = (size_t)t * a.H + h;
+            if constexpr (F32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                    if (h < a.H) v = *reinterpret_cast<const f32x4 *>((const float *)a.x + at + 4 * i);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) d[p][4 * i + q] = v[q];
+                }
+            } else {
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (h < a.H) v = *reinterpret_cast<const u32x4 *>((const uint16_t *)a.x + at);
+                unpack8<DT>(v, d[p]);
+            }
         }
         for (int j = 0; j < a.k; ++j) {
             const int r = rows[j];

@@ -29,6 +29,7 @@ MOE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "gba_moe.h")
 SCORES = {"softmax": 0, "sigmoid": 1}
 RENORMALIZE = 1
 POW2_SCALES = 1
+F32_TOKENS = 256
 
 _LIB = None
 
@@ -200,6 +201,13 @@ def moe_sort(indices, offsets, rows, slots=None, workspace=None):
 
 # --------------------------------------------------------- movement of rows ----
 
+def _tokens_dtype(y, tokens, *rest):
+    """The code of y's dtype, which rest share; tokens (combine's sums, or their gradient) may be float32 beside it."""
+    if tokens.dtype is torch.float32:
+        return _same_dtype(y, *rest) | F32_TOKENS
+    return _same_dtype(y, tokens, *rest)
+
+
 def moe_dispatch(x, rows, out):
     """out[rows[t, j]] = x[t]; other rows of out stay. x [T,H], rows int32 [T,k], out [R,H]. Returns out."""
     d = _device(x, rows, out)
@@ -214,9 +222,9 @@ def moe_dispatch(x, rows, out):
 
 def moe_combine(y, rows, weights, out):
     """out[t] = sum over j of weights[t, j] * y[rows[t, j]], slots of -1 left out; weights float32 [T,k], or None
-    for ones (the gradient of moe_dispatch). y [R,H], out [T,H]. Returns out."""
+    for ones (the gradient of moe_dispatch). y [R,H], out [T,H], of y's dtype or float32. Returns out."""
     d = _device(y, rows, weights, out)
-    dt = _same_dtype(y, out)
+    dt = _tokens_dtype(y, out)
     (R, H), (T, k) = y.shape, rows.shape
     _typed("rows", rows, torch.int32)
     _typed("weights", weights, torch.float32)
@@ -228,9 +236,10 @@ def moe_combine(y, rows, weights, out):
 
 def moe_combine_grad(dout, y, rows, weights, dy, dweights):
     """moe_combine's gradients: dy[rows[t, j]] = weights[t, j] * dout[t] (other rows stay) and dweights[t, j] =
-    <dout[t], y[rows[t, j]]>. Either of dy [R,H] and dweights (float32 [T,k]) may be None. Returns (dy, dweights)."""
+    <dout[t], y[rows[t, j]]>. dout [T,H] of y's dtype or float32; either of dy [R,H] and dweights (float32 [T,k]) may be
+    None. Returns (dy, dweights)."""
     d = _device(dout, y, rows, weights, dy, dweights)
-    dt = _same_dtype(dout, y, dy)
+    dt = _tokens_dtype(y, dout, dy)
     (R, H), (T, k) = y.shape, rows.shape
     _typed("rows", rows, torch.int32)
     _typed("weights", weights, torch.float32)
