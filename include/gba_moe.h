@@ -20,11 +20,14 @@
  *   - Unknown flag bits: GBA_ERR_SHAPE.
  *   - A launch failure returns GBA_ERR_HIP (gbm_last_hip_error() gives the
  *     code); a device that is not gfx950 GBA_ERR_DEVICE.
- *   - Results are the same bits in every run.
+ *   - Results are the same bits in every run (but for rows that two slots name, see below).
  *
  * Slots and rows. Token t's j-th expert, slot (t, j), is indices[t][j], or -1. Rows are
  * sorted by expert, rows of one expert by (t, j): expert e owns rows offsets[e] ..
  * offsets[e+1] - 1, the groups of gba_experts.h, and rows[t][j] is the row of slot (t, j), or -1.
+ * No row belongs to two slots, as moe_sort leaves rows: where a caller's own rows name one twice, calls that write rows
+ * (moe_dispatch, dy of moe_combine_grad, fp8_quantize) leave in it, place by place, a value of either slot, in another
+ * mixture in another run, and fp8_quantize may leave one slot's codes with the other's scales.
  * T k <= 2^29. Whatever indices and rows hold, nothing outside the arrays is touched: an
  * expert outside [0, E) or a row outside [0, R) counts as -1.
  */
@@ -89,8 +92,7 @@ size_t moe_sort_workspace(int64_t T, int64_t E, int64_t k);
 
 /* --------------------------------------------------------- movement of rows -- */
 
-/* out[rows[t][j]] = x[t]: x [T,H], out [R,H]. Rows of no slot are left as they were; a row named
- * twice holds one of the two. */
+/* out[rows[t][j]] = x[t]: x [T,H], out [R,H]. Rows of no slot are left as they were. */
 int moe_dispatch(const void *x, const int32_t *rows, void *out, int64_t T, int64_t k, int64_t H, int64_t R, int dtype);
 
 /* In the dtype of moe_combine and moe_combine_grad, beside the experts' rows' type: out and dout, the tokens' side,

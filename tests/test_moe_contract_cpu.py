@@ -1,0 +1,19 @@
+"""What the header and the docstrings say of cases that the code cannot settle, or settles in a way that a caller has to know."""
+import re
+
+import pytest
+
+import tiled_dense_gemm_bias_amd as gba
+
+
+@pytest.fixture(scope="module")
+def header():
+    """The header's comments as running text."""
+    return re.sub(r"\s*\n \*\s*", " ", open(gba.moe.MOE_HEADER).read())
+
+
+def test_rows_of_two_slots(header):
+    """Several waves write a row, in no order."""
+    assert "holds one of the two" not in header
+    assert "No row belongs to two slots" in header and "(but for rows that two slots name, see below)" in header
+    assert "mixture of both" in gba.moe.__doc__

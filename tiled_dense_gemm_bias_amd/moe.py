@@ -8,8 +8,9 @@ for the C ABI). The names here are also names of the package.
     gba.moe_combine(y, rows, weights, out)
 
 Slot (t, j) is token t's j-th expert; rows are sorted by expert, and rows[t, j] is the row of
-slot (t, j), or -1. As in the rest of the package the caller owns every tensor, work runs on the
-current stream, and tensors used on another stream than the one they were made on are the
+slot (t, j), or -1. A row belongs to one slot at most: one that a caller's own rows name twice is
+written as a mixture of both. As in the rest of the package the caller owns every tensor, work runs
+on the current stream, and tensors used on another stream than the one they were made on are the
 caller's to keep alive (torch's record_stream).
 """
 from __future__ import annotations
