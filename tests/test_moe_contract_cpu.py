@@ -17,3 +17,8 @@ def test_rows_of_two_slots(header):
     assert "holds one of the two" not in header
     assert "No row belongs to two slots" in header and "(but for rows that two slots name, see below)" in header
     assert "mixture of both" in gba.moe.__doc__
+
+
+def test_gradients_of_rows_without_a_slot(header):
+    assert "NaN where moe_route's weights are NaN for its logits" in header
+    assert "NaN where moe_route's weights are NaN" in " ".join(gba.moe_route_grad.__doc__.split())

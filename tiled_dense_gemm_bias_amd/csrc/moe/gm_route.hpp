@@ -593,6 +593,7 @@ constexpr int kGradWaves = 4;
 //   softmax:                dx_e = p_e (g_e [chosen] - D) for every expert
 //   sigmoid, renormalised:  dx_i = q_i (1 - s_i) (g_i - D)
 //   sigmoid:                dx_i = g_i s_i (1 - s_i)
+// Only softmax that is not renormalised reads all logits of a row; so do rows without any slot, for a NaN among them.
 // A row's chosen terms go through LDS to the lanes that hold the experts; reading and writing the logits
 // and their gradient once is what bounds it (16384 x 256 in fp32 7.7 us, 4.6 TB/s).
 template <int G, int P>
@@ -626,8 +627,16 @@ route_grad_kernel(RouteGrad a) {
     some = any_of<G>(some, first);
     const bool dense = a.score == SCORE_SOFTMAX && !a.renorm;
     float x[P], m = -__builtin_inff(), z = 0.0f;
+    if (dense || !some) load_logits<G, P>(a.x, a.dtype, row, l, a.E, x);
+    // A row without any slot: NaN where moe_route's weights are, else zeros.
+    float none = 0.0f;
+    if (!some) {
+        bool bad = false;
+#pragma unroll
+        for (int p = 0; p < P; ++p) bad |= x[p] != x[p] || (a.score == SCORE_SOFTMAX && x[p] == __builtin_inff());
+        none = any_of<G>(bad, first) ? __builtin_nanf("") : 0.0f;
+    }
     if (dense) {
-        load_logits<G, P>(a.x, a.dtype, row, l, a.E, x);
 #pragma unroll
         for (int p = 0; p < P; ++p) m = fmaxf(m, x[p]);
         m = all_reduce<G>(m, Max{});
@@ -670,7 +679,8 @@ route_grad_kernel(RouteGrad a) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         v[p] = terms[p * G + l];
-        if (dense) v[p] = some ? x[p] * by * (v[p] - d) : 0.0f;
+        if (dense) v[p] = x[p] * by * (v[p] - d);
+        v[p] = some ? v[p] : none;
     }
     const auto store = [&](auto dtype_c) __attribute__((always_inline)) {
         constexpr int DT = decltype(dtype_c)::value;

@@ -162,7 +162,8 @@ def moe_route(logits, indices, weights, bias=None, offsets=None, rows=None, slot
 
 def moe_route_grad(logits, indices, dweights, dlogits, score="softmax", renormalize=True, scale=1.0):
     """dlogits [T,E] (the logits' dtype) from dweights (float32 [T,k]): the gradient of moe_route's
-    weights, for the experts that it chose. Returns dlogits."""
+    weights, for the experts that it chose. A token without any slot gets zeros, or NaN where moe_route's weights are NaN for
+    its logits. Returns dlogits."""
     d = _device(logits, indices, dweights, dlogits)
     T, E = logits.shape
     k = indices.shape[-1]
