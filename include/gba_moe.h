@@ -78,7 +78,7 @@ int moe_route(const void *logits, const float *bias, int32_t *indices, float *we
  * (the choice itself has none, and neither has the bias). Experts that are not chosen get zeros, except
  * with softmax scores that are not renormalised. Slots of -1 add nothing. A token without any slot gets zeros, or
  * NaN where moe_route's weights are NaN for its logits (a NaN; softmax: or +inf), so that these do not pass for padding.
- * indices as moe_route leaves them (of an expert twice in one row the terms add up). */
+ * indices as moe_route leaves them (of an expert more than once in one row the terms add up, in the order of j). */
 int moe_route_grad(const void *logits, const int32_t *indices, const float *dweights, void *dlogits, int64_t T, int64_t E,
                    int64_t k, int score, float scale, int dtype, int flags);
 

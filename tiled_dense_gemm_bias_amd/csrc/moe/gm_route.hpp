@@ -665,15 +665,30 @@ route_grad_kernel(RouteGrad a) {
     }
     d = dense || a.renorm ? all_reduce<G>(d, Sum{}) : 0.0f;
     wave_sync();
+    bool again = false;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         if (e[c] < 0) continue;
         float v = g[c];
         if (!dense) v = q[c] * (v - d);
         if (a.score == SCORE_SIGMOID) v *= chosen_score(SCORE_SIGMOID, -xs[c], 0.0f);   // 1 - s
-        atomicAdd(&terms[e[c]], v);   // a repeated expert's terms add up
+        q[c] = v;
+        again |= atomicAdd(&terms[e[c]], v) != 0.0f;   // a repeated expert's terms add up
     }
     wave_sync();
+    if (any_of<G>(again, first)) {
+        // Of an expert that is there more than once: in the order of its slots, not in the atomics'.
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (e[c] >= 0) terms[e[c]] = 0.0f;
+        wave_sync();
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            for (int j = 0; j < G && c * G + j < a.k; ++j) {
+                if (l == j && e[c] >= 0) terms[e[c]] += q[c];
+                wave_sync();
+            }
+    }
     if (!live) return;
     float v[P];
 #pragma unroll
