@@ -347,12 +347,15 @@ __device__ __forceinline__ double fma_to(double p, double r, double c) {
     return d;
 }
 
-// e^d for d <= 0 in 64 bits, within 2^-46 (the keys keep 42): d = n ln 2 + r, |r| <= ln 2 / 2, and e^r by its series up
-// to r^11 (the next term is 2^-47).
+// ln 2 as the 64-bit number nearest to it and the one nearest to what that leaves.
+constexpr double kLn2 = 0.6931471805599453, kLn2Rest = 2.3190468138462996e-17;
+
+// e^d for d <= 0 in 64 bits, within 2^-46 (the keys keep 42): d = n ln 2 + r, |r| <= ln 2 / 2 (d - n kLn2 rounds once,
+// to 2^-54), and e^r by its series up to r^11 (the next term is 2^-47).
 __device__ __forceinline__ double exp_neg(double d) {
     const double c = __builtin_fmax(d, -800.0);
     const double n = __builtin_rint(c * 1.4426950408889634);
-    const double r = fma(n, -1.9082149292705877e-10, fma(n, -6.93147180369123816490e-01, c));
+    const double r = fma(n, -kLn2Rest, fma(n, -kLn2, c));
     double p = fma(1.0 / 39916800.0, r, 1.0 / 3628800.0);
     p = fma_to(p, r, 1.0 / 362880.0);
     p = fma_to(p, r, 1.0 / 40320.0);
