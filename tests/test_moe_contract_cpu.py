@@ -22,3 +22,10 @@ def test_rows_of_two_slots(header):
 def test_gradients_of_rows_without_a_slot(header):
     assert "NaN where moe_route's weights are NaN for its logits" in header
     assert "NaN where moe_route's weights are NaN" in " ".join(gba.moe_route_grad.__doc__.split())
+
+
+def test_slots_without_a_row_in_combine(header):
+    """An infinity or a NaN among their weights makes the token's sums NaN."""
+    doc = " ".join(gba.moe_combine.__doc__.split())
+    assert "left out" not in doc and "A slot of -1 adds its weight times 0" in doc
+    assert "A slot of -1 adds weight times 0" in header

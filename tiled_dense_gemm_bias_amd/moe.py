@@ -223,8 +223,9 @@ def moe_dispatch(x, rows, out):
 
 
 def moe_combine(y, rows, weights, out):
-    """out[t] = sum over j of weights[t, j] * y[rows[t, j]], slots of -1 left out; weights float32 [T,k], or None
-    for ones (the gradient of moe_dispatch). y [R,H], out [T,H], of y's dtype or float32. Returns out."""
+    """out[t] = sum over j of weights[t, j] * y[rows[t, j]]; weights float32 [T,k], or None for ones (the gradient of
+    moe_dispatch). A slot of -1 adds its weight times 0, so that weight has to be finite: moe_route leaves 0 there, and NaN in
+    rows whose logits hold a NaN, which then shows in out. y [R,H], out [T,H], of y's dtype or float32. Returns out."""
     d = _device(y, rows, weights, out)
     dt = _tokens_dtype(y, out)
     (R, H), (T, k) = y.shape, rows.shape
