@@ -215,8 +215,7 @@ f8_persist_kernel(Group g) {
     };
     read_first();
 
-    // Product q of a slice: column block q / 4, row blocks in alternating direction.
-    auto fm_of = [](int q) { return q % FM; };
+    // Product q of a slice: column block q / 4, row block q % 4.
     for (int r = 0;; ++r) {
         Tile nxt;
         const bool nxt_live = tile_of(r + 1, nxt);
@@ -278,7 +277,7 @@ f8_persist_kernel(Group g) {
 #pragma unroll
                 for (int p = NMF - LAG; p < NMF; ++p)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[p / FM][fm_of(p)][i] = 0.0f;
+                    for (int i = 0; i < 4; ++i) acc[p / FM][p % FM][i] = 0.0f;
             }
             st = other;
         };
@@ -289,7 +288,7 @@ f8_persist_kernel(Group g) {
         asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int p = NMF - LAG; p < NMF; ++p) scaled_add<false>(acc[p / FM][fm_of(p)], t[p % (LAG + 1)], s[fm_of(p)]);
+        for (int p = NMF - LAG; p < NMF; ++p) scaled_add<false>(acc[p / FM][p % FM], t[p % (LAG + 1)], s[p % FM]);
 
         // ---- epilogue, while the next tile's first slices land ----
         __builtin_amdgcn_sched_barrier(0);
