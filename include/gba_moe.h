@@ -143,10 +143,12 @@ int fp8_dequantize_weights(const void *codes, const float *scales, void *W, int6
 
 /* C = act(Z), Z = A.W^T + bias: A [M,K] in rows' form, W [N,K] in weights' form (E = 1); bias [N] or
  * NULL, C [M,N] and preact [M,N] or NULL (receives Z, rounded) in `dtype`. Each block's products are summed by the
- * matrix cores, scaled by both scales and added in fp32. The matrix cores' own rule, as measured: of each 8 consecutive
- * products, those with less than 2^-13 of the largest's power of two lose what is below that, towards zero. K a multiple of 16, at most 2^22; N of 8, at most 2^23; M at
- * most 2^29. K = 0 gives act(bias). workspace: NULL, or device memory (16-byte aligned) that lets calls with
- * few output tiles split K (deterministic; contents neither needed nor kept). */
+ * matrix cores, multiplied by the two scales' product and added, in fp32: a scales' product below 2^-126 has fewer bits,
+ * one of 2^128 or more is an infinity (blocks whose largest values' product is beyond 2^145). The matrix cores' own
+ * rule, as measured: of each 8 consecutive products, those with less than 2^-13 of the largest's power of two lose what
+ * is below that, towards zero. K a multiple of 16, at most 2^22; N of 8, at most 2^23; M at most 2^29. K = 0 gives
+ * act(bias). workspace: NULL, or device memory (16-byte aligned) that lets calls with few output tiles split K
+ * (deterministic; contents neither needed nor kept). */
 int gemm_bias_act_fp8_block(const void *a_codes, const float *a_scales, const void *w_codes, const float *w_scales,
                             const void *bias, void *C, void *preact, int64_t M, int64_t N, int64_t K, int act, int dtype,
                             void *workspace, size_t workspace_bytes);

@@ -29,3 +29,7 @@ def test_slots_without_a_row_in_combine(header):
     doc = " ".join(gba.moe_combine.__doc__.split())
     assert "left out" not in doc and "A slot of -1 adds its weight times 0" in doc
     assert "A slot of -1 adds weight times 0" in header
+
+
+def test_range_of_the_scales_product(header):
+    assert "a scales' product below 2^-126 has fewer bits, one of 2^128 or more is an infinity" in header
