@@ -63,6 +63,8 @@ enum { GBM_RENORMALIZE = 1 };                   /* flags of moe_route and its gr
  *   chosen experts' sum with GBM_RENORMALIZE.
  * Equal values: the lower number first, for experts and groups alike. Values are compared as 64-bit
  * numbers (cut to 42 bits), the logits themselves where neither a bias nor group_best = 2 is involved.
+ * Weights are formed in fp32 from the chosen logits: off by up to (2 D + 40) 2^-24 of themselves, D the largest distance of a
+ * logit from the row's largest (softmax) or the largest logit's magnitude (sigmoid).
  * An expert whose logit or bias is -inf is never chosen: a slot that no expert is left for has index -1
  * and weight 0 (a padding token's logits are all -inf). A row with a NaN (softmax: or a logit of +inf; or a
  * NaN in the bias) has indices -1 and weights NaN.

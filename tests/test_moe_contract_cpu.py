@@ -33,3 +33,12 @@ def test_slots_without_a_row_in_combine(header):
 
 def test_range_of_the_scales_product(header):
     assert "a scales' product below 2^-126 has fewer bits, one of 2^128 or more is an infinity" in header
+
+
+def test_accuracy_of_routing_weights(header):
+    """What tests/moe_oracle.py's route_tol holds them to."""
+    assert "off by up to (2 D + 40) 2^-24 of themselves" in header
+    import torch
+    from tests import moe_oracle as orc
+    w, depth = torch.tensor([[0.5]], dtype=torch.float64), torch.tensor([3.0], dtype=torch.float64)
+    assert abs(orc.route_tol(w, depth).item() - 46 * 2.0 ** -25) < 2.0 ** -100
