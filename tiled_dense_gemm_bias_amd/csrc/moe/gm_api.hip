@@ -260,9 +260,11 @@ int moe_route(const void *logits, const float *bias, int32_t *indices, float *we
         a.renorm = (flags & GBM_RENORMALIZE) != 0;
         a.dtype = dtype;
         a.scale = scale;
-        // One block that sorts as well, where its waves are few enough (8 tokens of 256 grouped experts 10 us, by two kernels
-        // 11 to 12; 64 of 128 experts 10, by two kernels 7 to 9).
-        const bool fused = sort && !counted && E <= 256 && (T <= 32 || (E <= 32 && T <= gbm::kRouteWaves * 4));
+        // One block that sorts as well, where its waves are few enough. One block and two kernels, us: up to 16 tokens 4.2 to 10.5 and
+        // 5.5 to 11.6 for any E (256 grouped experts 10.5, 11.6). 32 tokens: 32 experts 5.2, 6.3; 64 5.8, 6.7; 128 7.1, 7.5 (16
+        // slots each 7.9, 8.3; grouped 9.5, 9.4), but 160 10.5, 9.8; 256 10.2, 9.4; grouped 13.2, 12.0. 64 tokens: 16 experts 5.3, 6.1;
+        // 32 6.1, 6.4 (16 slots 8.3, 7.5), but 64 7.2, 6.7; 128 9.5, 7.5.
+        const bool fused = sort && !counted && E <= 256 && T <= (E <= 32 ? gbm::kRouteWaves * 4 : E <= 128 ? 32 : 16);
         a.tokens = fused ? (int)T : counted ? order.per_block / (int)k : kLeastTokens;
         // Grouped keys fill a CU's LDS for 16 waves, however many work: as many as there are tokens for (16384 x 256 31 us with four).
         if (groups > top_groups && E > 64 && !fused && !counted)
