@@ -1,9 +1,11 @@
-"""Routing on both sides of the sizes where one launch becomes two."""
+"""Routing and combine's gradients on both sides of the sizes where one launch becomes two, and where a token's waves change."""
 import math
 
 import pytest
 
 from tests.gpu_util import say
+from tests.test_gpu_moe_f32 import test_gradients as combine_grad_f32
+from tests.test_gpu_moe_move import test_combine_grad as combine_grad
 from tests.test_gpu_moe_route import check, logits
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +32,16 @@ def test_routed(T, E, k, groups, top, score):
     bias = torch.randn(E, generator=g, device="cuda") * 0.1
     check(x, k, bias, score=score, groups=groups, top_groups=top, group_best=2 if groups > 1 else 1)
     check(x.bfloat16(), k, None, score=score, groups=groups, top_groups=top, renormalize=False)
+
+
+# Tokens, slots, columns, rows: around the sizes where a token gets four waves, or one.
+GRADIENTS = [(512, 3, 1024, 1700), (513, 3, 1024, 1700), (1024, 2, 2048, 2100), (1025, 2, 2048, 2100), (513, 9, 1032, 4000), (2304, 1, 2056, 2600),
+             (2305, 1, 2056, 2600), (2049, 1, 3584, 2049), (3001, 1, 4096, 3001)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,k,H,R", GRADIENTS)
+def test_combine_gradients(T, k, H, R, dtype):
+    for weighted in (True, False):
+        combine_grad(T, k, H, R, dtype, weighted)
+        combine_grad_f32(T, k, H, R, dtype, weighted)

@@ -107,9 +107,14 @@ constexpr int kGradPieces = 4, kMaxSlots = 32;   // pieces of eight columns that
 
 // W waves a token, 4 / W tokens a workgroup. Where tokens are many and their rows short of 4096 one wave a token is faster, as
 // all its lanes have columns (4 slots, a wave and four: 65536 x 512 132 and 403 us, 32768 x 1024 110 and 242, 16384 x 2048 114
-// and 150, 8192 x 2816 82 and 88, 8192 x 4096 114 both, 8192 x 7168 200 and 193); few tokens want more waves each (8 slots, 1000 x
-// 2048: 23 and 19). The next slot's row loaded ahead took longer everywhere (16384 x 2048 115; twice the registers).
-inline bool one_wave_a_token(long long T, int H) { return T >= 2048 && H < 4096; }
+// and 150, 8192 x 2816 82 and 88, 8192 x 4096 114 both, 8192 x 7168 200 and 193); few tokens want more waves each, and the fewer
+// the columns the earlier they have enough: 4 slots, a wave and four: of 128 columns 512 tokens 5.6 and 5.8, 1500 6.3 and 10.2; 1024
+// columns 256 7.0 and 6.8, 512 8.0 both, 1500 10.3 and 15.5; 2048 columns 1000 13.0 and 11.8, 1500 15.1 and 18.3; 2816 columns 1500
+// 23.5 and 21.1, 2048 26.5 and 24.8, 2500 30.0 and 31.4; 3584 columns 2048 28.9 and 28.4, 3000 38.5 and 39.8. (With 1, 2 and 8
+// slots the same within 10 %: 8 slots of 1024 columns 512 13.9 and 13.7, 768 14.9 and 15.4; 2048 columns 1000 23.3 and 19.7, 1200 25.4
+// and 29.6; 1 slot of 2816 2048 10.2 both.) The next slot's row loaded ahead took longer everywhere (16384 x 2048 115; twice
+// the registers).
+inline bool one_wave_a_token(long long T, int H) { return T > (H <= 1024 ? 512 : H <= 2048 ? 1024 : 2304) && H < 4096; }
 
 // F32: dout as combine's sums, in 32 bits.
 template <int DT, int W, bool F32>
