@@ -85,7 +85,8 @@ int moe_route_grad(const void *logits, const int32_t *indices, const float *dwei
                    int64_t k, int score, float scale, int dtype, int flags);
 
 /* offsets [E+1] and rows [T,k] of indices [T,k], by a stable sort; slots [T k] or NULL: the slot t k + j of each
- * row, -1 for the rows from offsets[E] on. workspace: moe_sort_workspace bytes, 16-byte aligned
+ * row, -1 for the rows from offsets[E] on. k may be more than E, as where one device holds some of a token's experts and the
+ * others' slots are -1. workspace: moe_sort_workspace bytes, 16-byte aligned
  * (GBA_ERR_SCRATCH if less; contents neither needed nor kept). T = 0: offsets of zeros. */
 int moe_sort(const int32_t *indices, int32_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int64_t E, int64_t k,
              void *workspace, size_t workspace_bytes);

@@ -86,9 +86,10 @@ size_t size3(int64_t a, int64_t b, int64_t c) { return (size_t)a * (size_t)b * (
 // Rows and slots are 32-bit numbers; a row's length leaves room for a tile's 32-bit byte offsets.
 constexpr int64_t kMaxRows = 1LL << 29, kMaxWidth = 1LL << 23, kMaxDepth = 1LL << 22;
 
-bool bad_route(int64_t T, int64_t E, int64_t k) {
-    return T < 0 || E < 1 || E > gbm::kMaxExperts || k < 1 || k > gbm::kMaxTop || k > E || T > kMaxRows / k;
+bool bad_sort(int64_t T, int64_t E, int64_t k) {
+    return T < 0 || E < 1 || E > gbm::kMaxExperts || k < 1 || k > gbm::kMaxTop || T > kMaxRows / k;
 }
+bool bad_route(int64_t T, int64_t E, int64_t k) { return bad_sort(T, E, k) || k > E; }
 
 // ------------------------------------------------------------------- sorting --
 
@@ -212,7 +213,7 @@ int gbm_set_stream(void *s) {
     return GBA_OK;
 }
 
-size_t moe_sort_workspace(int64_t T, int64_t E, int64_t k) { return bad_route(T, E, k) ? 0 : sort_bytes(T, E, k); }
+size_t moe_sort_workspace(int64_t T, int64_t E, int64_t k) { return bad_sort(T, E, k) ? 0 : sort_bytes(T, E, k); }
 
 int moe_route(const void *logits, const float *bias, int32_t *indices, float *weights, int32_t *offsets, int32_t *rows, int32_t *slots,
               int64_t T, int64_t E, int64_t k, int64_t groups, int64_t top_groups, int group_best, int score, float scale, int dtype,
@@ -306,7 +307,7 @@ int moe_route_grad(const void *logits, const int32_t *indices, const float *dwei
 
 int moe_sort(const int32_t *indices, int32_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int64_t E, int64_t k, void *workspace,
              size_t workspace_bytes) {
-    if (bad_route(T, E, k)) return GBA_ERR_SHAPE;
+    if (bad_sort(T, E, k)) return GBA_ERR_SHAPE;
     const Span spans[] = {{indices, size3(T, k, 4), true, false, 4},
                           {offsets, size3(E + 1, 4, 1), true, true, 4},
                           {rows, size3(T, k, 4), true, true, 4},
