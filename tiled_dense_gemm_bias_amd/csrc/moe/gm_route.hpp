@@ -17,10 +17,10 @@
 // ratios that do not underflow together: s_i e^-min(m, 0), m the largest chosen logit.
 //
 // What bounds it: vector instructions, and the latency of small kernels. 16384 rows of 256 fp32 logits with a
-// bias, k = 8, are 17 MB (3.3 us at 5.1 TB/s) and take 15 us: 1400 vector instructions a wave of four rows are 71 % of its
+// bias, k = 8, are 17 MB (3.3 us at 5.1 TB/s) and take 15 us: 1400 vector instructions a wave of four rows are 70 % of its
 // time (a quarter each for the exponentials and the k rounds). 999 rows of grouped experts take 10 us, 8 rows of 32 experts with
 // their sorting, all in one workgroup, 3.8 us. As many values in a lane as its registers take (16), as the rounds are a wave's
-// and not a value's: 8192 rows of 384 experts take 9.9 us in 32 lanes each and 13.7 in 64 (with a bias 16.0 and 19.2).
+// and not a value's: 8192 rows of 384 experts take 10.5 us in 32 lanes each and 13.8 in 64 (with a bias 15 and 19).
 #pragma once
 
 #include "gm_common.hpp"
@@ -599,7 +599,7 @@ constexpr int kGradWaves = 4;
 //   sigmoid:                dx_i = g_i s_i (1 - s_i)
 // Only softmax that is not renormalised reads all logits of a row; so do rows without any slot, for a NaN among them.
 // A row's chosen terms go through LDS to the lanes that hold the experts; reading and writing the logits
-// and their gradient once is what bounds it (16384 x 256 in fp32 7.7 us, 4.6 TB/s).
+// and their gradient once is what bounds it (16384 x 256 in fp32 8.3 us, 4.1 TB/s; renormalised 7.5).
 template <int G, int P>
 __global__ void __launch_bounds__(kGradWaves * 64)
 route_grad_kernel(RouteGrad a) {
