@@ -1,4 +1,4 @@
-"""The persistent kernel of the 8-bit products at the sizes of moe_cases.LARGE, each of which is asserted to be taken by it:
+"""The persistent kernel of the 8-bit products at the sizes of moe_large_cases.LARGE, each of which is asserted to be taken by it:
 against the 64-bit definition, bit for bit on whole numbers, with NaN scales and with offsets that reach outside the rows."""
 import math
 
@@ -6,7 +6,8 @@ import pytest
 
 import tiled_dense_gemm_bias_amd as gba
 from tests import experts_oracle as eo
-from tests import moe_cases as cases
+from tests import moe_cases
+from tests import moe_large_cases as cases
 from tests import moe_oracle as orc
 from tests.gpu_util import say
 from tests.test_gpu_experts import draw, make_offsets
@@ -107,7 +108,7 @@ def test_a_scale_of_nan_stays_in_its_rows_and_columns(T, E, N, K):
     say("large nan", T, E, N, K)
     assert persistent(T, E, N, K)
     g = torch.Generator(device="cuda").manual_seed(8)
-    sizes = cases.shares(T, E, T + N)
+    sizes = moe_cases.shares(T, E, T + N)
     first = next(e for e in range(E) if sizes[e])
     x, w = draw(g, (T, K), torch.bfloat16), draw(g, (E, N, K), torch.bfloat16, K ** -0.5)
     x[1, K - 3] = x[T - 1, 0] = math.nan

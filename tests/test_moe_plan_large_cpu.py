@@ -1,7 +1,7 @@
 """The sizes of the persistent 8-bit kernel's tests are ones that it takes, and reach what they are for, without a GPU."""
 import pytest
 
-from tests import moe_cases as cases
+from tests import moe_large_cases as cases
 from tests import test_gpu_fp8_block_large as large
 from tiled_dense_gemm_bias_amd import moe
 
